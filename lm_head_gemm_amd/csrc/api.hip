@@ -5,7 +5,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "fs_common.h"
+#include "fs_decode.h"
 
 // Workspace of fs_sample_fused_noalloc: a static device array, one copy per
 // GPU at that GPU's own address. Host code never uses this name as an
@@ -14,9 +14,15 @@
 static __device__ __align__(256) unsigned char scratch[FS_NOALLOC_SCRATCH_BYTES];
 
 namespace fs {
-namespace {
 
-thread_local int g_last_hip_error = 0;
+static thread_local int g_last_hip_error = 0;
+
+fs_status_t fail_hip(hipError_t e) {
+  g_last_hip_error = (int)e;
+  return FS_ERR_HIP;
+}
+
+namespace {
 
 constexpr int64_t kMaxB = 65536;
 constexpr int64_t kMaxV = 0x7FFFFFFF;       // tokens are int32
@@ -56,11 +62,6 @@ bool dtype_ok(int t) { return t == FS_DTYPE_BF16 || t == FS_DTYPE_F32; }
 
 bool sizes_ok(int64_t B, int64_t D, int64_t V) {
   return B > 0 && D > 0 && V > 0 && B <= kMaxB && D <= kMaxD && V <= kMaxV;
-}
-
-fs_status_t fail_hip(hipError_t e) {
-  g_last_hip_error = (int)e;
-  return FS_ERR_HIP;
 }
 
 struct Plan {

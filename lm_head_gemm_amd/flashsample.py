@@ -1,12 +1,14 @@
 """Python binding of libflashsample (argument marshalling only).
 
-Every step of sampling runs in the library's HIP kernels; PyTorch supplies
-device memory and the current stream. The function names follow the C ABI in
-include/flashsample.h. Importing this module loads the library and fails
+Every step of sampling, of the 8-bit head and of beam search runs in the
+library's HIP kernels; PyTorch supplies device memory and the current stream.
+The function names follow the C ABI in include/flashsample.h and
+include/flashsample_decode.h. Importing this module loads the library and fails
 loudly if it has not been built (python -m lm_head_gemm_amd.build).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -49,6 +51,15 @@ class FsOptions(ctypes.Structure):
         ("group_size", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
     ]
+
+
+FS_BEAM_MAX = 64
+FS_BEAM_MAX_STATES = 192
+
+
+class FsBeamLayout(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in
+                ("outer", "outer_stride", "row_stride", "blocks", "block_stride", "block_bytes")]
 
 
 class FlashSampleError(RuntimeError):
@@ -107,6 +118,27 @@ def _load():
     lib.fs_probe_read_blocks.argtypes = [c_i64, c_i64]
     lib.fs_probe_read.restype = ctypes.c_int
     lib.fs_probe_read.argtypes = [vp, c_i64, c_i64, vp, vp]
+    lib.fs_quantize_i8.restype = ctypes.c_int
+    lib.fs_quantize_i8.argtypes = [vp, c_i64, ctypes.c_int, c_i64, c_i64, vp, c_i64, vp, vp]
+    lib.fs_rms_norm_i8.restype = ctypes.c_int
+    lib.fs_rms_norm_i8.argtypes = [vp, c_i64, vp, c_i64, vp, ctypes.c_int, ctypes.c_int, c_i64, c_i64,
+                                   ctypes.c_float, vp, c_i64, vp, c_i64, vp, vp]
+    product = [vp, c_i64, vp, vp, c_i64, vp, c_i64, c_i64, c_i64]
+    lib.fs_matmul_i8.restype = ctypes.c_int
+    lib.fs_matmul_i8.argtypes = product + [vp, c_i64, ctypes.c_int, vp]
+    lib.fs_sample_i8_workspace_bytes.restype = c_sz
+    lib.fs_sample_i8_workspace_bytes.argtypes = [c_i64, c_i64, c_i64]
+    lib.fs_sample_i8.restype = ctypes.c_int
+    lib.fs_sample_i8.argtypes = product + [ctypes.c_float, c_u64, c_u64, vp, c_sz, vp, vp]
+    lib.fs_beam_select_workspace_bytes.restype = c_sz
+    lib.fs_beam_select_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64]
+    lib.fs_beam_select.restype = ctypes.c_int
+    lib.fs_beam_select.argtypes = [vp, c_i64, ctypes.c_int, vp, vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_i64,
+                                   vp, c_sz, vp, vp, vp, vp]
+    layout = ctypes.POINTER(FsBeamLayout)
+    lib.fs_beam_reorder.restype = ctypes.c_int
+    lib.fs_beam_reorder.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), c_i64, layout, layout, vp, c_i64,
+                                    c_i64, vp]
     return lib
 
 
@@ -315,3 +347,294 @@ def probe_read(src: torch.Tensor, chunk_bytes: int = 1 << 19, sink: torch.Tensor
     _check(_lib.fs_probe_read(src.data_ptr(), nbytes, chunk_bytes, sink.data_ptr(), _stream(stream)),
            "fs_probe_read")
     return sink
+
+
+# ------------------------------------------------------- 8-bit head, beam search
+def _on(device: torch.device, stream):
+    """Where a call on tensors of `device` allocates and launches: on `stream`
+    (a torch stream of that device), or on that device's current stream. What
+    is allocated within belongs to that stream, so its memory is not handed on
+    while the call still runs there."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _same_device(x: torch.Tensor, *others) -> torch.device:
+    if not x.is_cuda:
+        raise ValueError("device tensors expected")
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"tensors on one device expected, got {x.device} and {t.device}")
+    return x.device
+
+
+def _expect(t: torch.Tensor, shape, dtype, what: str, rows: bool = True):
+    """A tensor of this shape and dtype; contiguous rows (2-D) or elements."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if (t.dim() == 2 and rows and t.shape[1] > 1 and t.stride(1) != 1) or \
+            ((t.dim() == 1 or not rows) and not t.is_contiguous()):
+        raise ValueError(f"{what}: contiguous {'rows' if t.dim() == 2 and rows else 'elements'} expected")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor with contiguous rows (torch leaves the
+    stride of a single row open)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _rows(x: torch.Tensor, what="x"):
+    if x.dim() != 2:
+        raise ValueError(f"{what}: [rows, columns] expected, got {tuple(x.shape)}")
+    _expect(x, x.shape, x.dtype, what)
+    return x.shape
+
+
+def _codes(x, q, scales):
+    M, D = x.shape
+    if q is None:
+        q = torch.empty((M, D), dtype=torch.int8, device=x.device)
+    else:
+        _expect(q, (M, D), torch.int8, "q")
+    if scales is None:
+        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        _expect(scales, (M,), torch.float32, "scales")
+    return q, scales
+
+
+def quantize_i8(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """Rows of x [M, D] (bf16 or fp32) as 8-bit codes and one scale per row:
+    (q int8 [M, D], scales fp32 [M]) with x ~ q * scales[:, None]
+    (fs_quantize_i8). Brings an LM head [V, D] to 8 bits (once, when it is
+    loaded) and hidden states that are normed already."""
+    M, D = _rows(x)
+    dt = _dtype_code(x.dtype)
+    with _on(_same_device(x, q, scales), stream):
+        q, scales = _codes(x, q, scales)
+        st = _lib.fs_quantize_i8(x.data_ptr(), _ld(x), dt, M, D, q.data_ptr(), _ld(q), scales.data_ptr(),
+                                 _stream(None))
+    _check(st, "fs_quantize_i8")
+    return q, scales
+
+
+def rms_norm_i8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                sum_out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                scales: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of x (+ residual), times gain [D], as 8-bit codes
+    and one scale per row (fs_rms_norm_i8): (q, scales), and with a residual
+    (q, scales, h), h = x + residual in x's dtype. h goes to sum_out if given,
+    which may be x or residual itself. gain is in x's dtype or fp32."""
+    M, D = _rows(x)
+    dt = _dtype_code(x.dtype)
+    _expect(gain, (D,), gain.dtype, "gain")
+    gt = _dtype_code(gain.dtype)
+    if residual is not None:
+        _expect(residual, (M, D), x.dtype, "residual")
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual")
+    with _on(_same_device(x, gain, residual, sum_out, q, scales), stream):
+        if residual is not None:
+            if sum_out is None:
+                sum_out = torch.empty((M, D), dtype=x.dtype, device=x.device)
+            else:
+                _expect(sum_out, (M, D), x.dtype, "sum_out")
+        q, scales = _codes(x, q, scales)
+        st = _lib.fs_rms_norm_i8(x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(),
+                                 0 if residual is None else _ld(residual), gain.data_ptr(), gt, dt, M, D, float(eps),
+                                 None if residual is None else sum_out.data_ptr(),
+                                 0 if residual is None else _ld(sum_out), q.data_ptr(), _ld(q), scales.data_ptr(),
+                                 _stream(None))
+    _check(st, "fs_rms_norm_i8")
+    return (q, scales) if residual is None else (q, scales, sum_out)
+
+
+def _product_inputs(q, q_scales, w, w_scales):
+    M, K = _rows(q, "q")
+    N = w.shape[0]
+    _expect(q, (M, K), torch.int8, "q")
+    _expect(w, (N, K), torch.int8, "w")
+    _expect(q_scales, (M,), torch.float32, "q_scales")
+    _expect(w_scales, (N,), torch.float32, "w_scales")
+    return M, N, K
+
+
+def matmul_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+              out: torch.Tensor | None = None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """(q * q_scales[:, None]) @ (w * w_scales[:, None]).T of 8-bit codes q
+    [M, K] and w [N, K], summed exactly in integers (fs_matmul_i8): [M, N] in
+    out's dtype, or out_dtype (bf16 or fp32). K is a multiple of 16."""
+    M, N, K = _product_inputs(q, q_scales, w, w_scales)
+    with _on(_same_device(q, q_scales, w, w_scales, out), stream):
+        if out is None:
+            dt = _dtype_code(out_dtype)
+            out = torch.empty((M, N), dtype=out_dtype, device=q.device)
+        else:
+            _expect(out, (M, N), out.dtype, "out")
+            dt = _dtype_code(out.dtype)
+        st = _lib.fs_matmul_i8(q.data_ptr(), _ld(q), q_scales.data_ptr(), w.data_ptr(), _ld(w), w_scales.data_ptr(),
+                               M, N, K, out.data_ptr(), _ld(out), dt, _stream(None))
+    _check(st, "fs_matmul_i8")
+    return out
+
+
+def sample_i8_workspace_bytes(B, D, V) -> int:
+    return int(_lib.fs_sample_i8_workspace_bytes(B, D, V))
+
+
+def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, temperature: float,
+              seed: int, step: int, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """One token per row from softmax(l / T), l = matmul_i8's fp32 logits of
+    codes q [B, D] and an 8-bit LM head w [V, D] (fs_sample_i8). Noise, ties
+    and NaN rule are sample_fused's."""
+    B, V, D = _product_inputs(q, q_scales, w, w_scales)
+    with _on(_same_device(q, q_scales, w, w_scales, out, workspace), stream):
+        if out is None:
+            out = torch.empty(B, dtype=torch.int32, device=q.device)
+        else:
+            _expect(out, (B,), torch.int32, "out")
+        if workspace is None:
+            workspace = torch.empty(max(sample_i8_workspace_bytes(B, D, V), 256), dtype=torch.uint8, device=q.device)
+        st = _lib.fs_sample_i8(q.data_ptr(), _ld(q), q_scales.data_ptr(), w.data_ptr(), _ld(w), w_scales.data_ptr(),
+                               B, D, V, float(temperature), int(seed), int(step), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), out.data_ptr(), _stream(None))
+    _check(st, "fs_sample_i8")
+    return out
+
+
+def beam_select_workspace_bytes(B, beams, V, n) -> int:
+    return int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None,
+                finished: torch.Tensor | None = None, pad_token: int = 0, out=None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """The n best continuations (default: as many as beams) of each group of
+    beams, from logits [B * beams, V] (bf16 or fp32) and scores fp32
+    [B, beams]: (scores fp32, parents int32, tokens int32), each [B, n], best
+    first (fs_beam_select). A beam marked in finished (bool or uint8
+    [B, beams]) stands for itself once, with pad_token. out: the three output
+    tensors."""
+    if scores.dim() != 2:
+        raise ValueError(f"scores [B, beams] expected, got {tuple(scores.shape)}")
+    B, beams = scores.shape
+    _expect(scores, (B, beams), torch.float32, "scores", rows=False)
+    if logits.dim() != 2 or logits.shape[0] != B * beams:
+        raise ValueError(f"logits [{B * beams}, V] expected, got {tuple(logits.shape)}")
+    _rows(logits, "logits")
+    dt = _dtype_code(logits.dtype)
+    V = logits.shape[1]
+    n = beams if n is None else int(n)
+    if finished is not None:
+        if finished.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"finished: bool or uint8 expected, got {finished.dtype}")
+        _expect(finished, (B, beams), finished.dtype, "finished", rows=False)
+    given = out if out is not None else ()
+    with _on(_same_device(logits, scores, finished, workspace, *given), stream):
+        if out is None:
+            out = (torch.empty((B, n), dtype=torch.float32, device=logits.device),
+                   torch.empty((B, n), dtype=torch.int32, device=logits.device),
+                   torch.empty((B, n), dtype=torch.int32, device=logits.device))
+        else:
+            for t, dtype, what in zip(out, (torch.float32, torch.int32, torch.int32),
+                                      ("out scores", "out parents", "out tokens"), strict=True):
+                _expect(t, (B, n), dtype, what, rows=False)
+        if workspace is None:
+            nbytes = beam_select_workspace_bytes(B, beams, V, n)
+            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=logits.device)
+        st = _lib.fs_beam_select(logits.data_ptr(), _ld(logits), dt, scores.data_ptr(),
+                                 None if finished is None else finished.data_ptr(), int(pad_token), B, beams, V, n,
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _stream(None))
+    _check(st, "fs_beam_select")
+    return tuple(out)
+
+
+def _fold(dims):
+    """Dimensions (size, stride in bytes) from the outermost in, joined where
+    the next one continues the one before, those of size 1 left out."""
+    folded = []
+    for size, stride in dims:
+        if size == 1:
+            continue
+        if folded and folded[-1][1] == size * stride:
+            folded[-1] = (folded[-1][0] * size, stride)
+        else:
+            folded.append((size, stride))
+    return folded
+
+
+def _beam_layout(t: torch.Tensor, dim: int):
+    """(FsBeamLayout, byte offsets of the slabs that it does not reach) of a
+    state tensor whose rows are dimension dim."""
+    e = t.element_size()
+    dims = [(n, s * e) for n, s in zip(t.shape, t.stride())]
+    outer, inner = _fold(dims[:dim]), _fold(dims[dim + 1:] + [(e, 1)])
+    if inner and inner[-1][1] != 1:
+        raise ValueError(f"beam_reorder: strides {t.stride()} of {tuple(t.shape)} are not supported")
+    block = inner.pop()[0] if inner else 1
+    if len(inner) > 1:
+        raise ValueError(f"beam_reorder: strides {t.stride()} of {tuple(t.shape)} leave more than one run of blocks")
+    blocks = inner[0] if inner else (1, 0)
+    starts = [0]
+    for n, s in outer[:-1]:
+        starts = [o + i * s for o in starts for i in range(n)]
+    slab = outer[-1] if outer else (1, 0)
+    return FsBeamLayout(slab[0], slab[1], dims[dim][1], blocks[0], blocks[1], block), starts
+
+
+def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=None):
+    """Row b * beams + i of every state becomes the former row
+    b * beams + parents[b, i] (fs_beam_reorder). states: a tensor, or a list
+    of tensors of one shape, strides and dtype (say each layer's keys and
+    values), with B * beams rows in dimension dim; views are welcome, so a
+    cache is passed as far as it is filled (cache[:, :, :length]). parents:
+    int32 [B, beams]; a row whose parent is not in 0 .. beams - 1 stays as it
+    is. out: None (in place), or like states. Returns what was written."""
+    single = isinstance(states, torch.Tensor)
+    tensors = [states] if single else list(states)
+    targets = tensors if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
+    if parents.dim() != 2:
+        raise ValueError(f"parents [B, beams] expected, got {tuple(parents.shape)}")
+    B, beams = parents.shape
+    _expect(parents, (B, beams), torch.int32, "parents", rows=False)
+    if not tensors:
+        raise ValueError("no states")
+    if len(targets) != len(tensors):
+        raise ValueError(f"{len(tensors)} states and {len(targets)} outputs")
+    first = tensors[0]
+    dim = dim + first.dim() if dim < 0 else dim
+    if not 0 <= dim < first.dim() or first.shape[dim] != B * beams:
+        raise ValueError(f"states with {B * beams} rows in dimension {dim} expected, got {tuple(first.shape)}")
+    for group, like in ((tensors, first), (targets, targets[0])):
+        for t in group:
+            if t.shape != first.shape or t.dtype != first.dtype or t.stride() != like.stride():
+                raise ValueError("states (and outputs) of one shape, strides and dtype expected")
+    device = _same_device(first, parents, *tensors, *targets)
+    if first.numel() == 0:
+        return targets[0] if single else targets
+    layout, starts = _beam_layout(first, dim)
+    src = [t.data_ptr() + s for t in tensors for s in starts]
+    to, dst = layout, src
+    if targets is not tensors:
+        to, to_starts = _beam_layout(targets[0], dim)
+        dst = [t.data_ptr() + s for t in targets for s in to_starts]
+        if dst == src:
+            to, dst = layout, src
+        elif (to.outer, to.blocks, to.block_bytes) != (layout.outer, layout.blocks, layout.block_bytes):
+            raise ValueError("beam_reorder: the outputs' strides split the rows differently from the states'")
+    if len(src) > FS_BEAM_MAX_STATES:
+        raise ValueError(f"beam_reorder: more than {FS_BEAM_MAX_STATES} separate buffers in one call")
+    table = ctypes.c_void_p * len(src)
+    with _on(device, stream):
+        st = _lib.fs_beam_reorder(table(*src), None if dst is src else table(*dst), len(src), ctypes.byref(layout),
+                                  None if dst is src else ctypes.byref(to), parents.data_ptr(), B, beams,
+                                  _stream(None))
+    _check(st, "fs_beam_reorder")
+    return targets[0] if single else targets

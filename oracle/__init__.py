@@ -23,6 +23,8 @@ Modules:
   grouped  the grouped (hierarchical) variant: per vocabulary group a local
            sample and a local log-mass, then a Gumbel-max draw of the group
            from its own noise stream.
+  decode   the 8-bit head (codes, norm, product) and beam search (selection,
+           reordering).
 
 Every function is pinned by a CPU test against something other than itself
 (rocRAND's Philox for the words, closed forms of the Gumbel law, exact
@@ -48,3 +50,4 @@ from .grouped import (  # noqa: F401
     log_mass,
     sample_grouped,
 )
+from . import decode  # noqa: F401
