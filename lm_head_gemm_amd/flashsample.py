@@ -597,8 +597,7 @@ def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=N
     cache is passed as far as it is filled (cache[:, :, :length]). parents:
     int32 [B, beams]; a row whose parent is not in 0 .. beams - 1 stays as it
     is. out: None (in place), or like states. Returns what was written."""
-    single = isinstance(states, torch.Tensor)
-    tensors = [states] if single else list(states)
+    tensors = [states] if isinstance(states, torch.Tensor) else list(states)
     targets = tensors if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
     if parents.dim() != 2:
         raise ValueError(f"parents [B, beams] expected, got {tuple(parents.shape)}")
@@ -617,8 +616,9 @@ def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=N
             if t.shape != first.shape or t.dtype != first.dtype or t.stride() != like.stride():
                 raise ValueError("states (and outputs) of one shape, strides and dtype expected")
     device = _same_device(first, parents, *tensors, *targets)
+    written = states if out is None else out
     if first.numel() == 0:
-        return targets[0] if single else targets
+        return written
     layout, starts = _beam_layout(first, dim)
     src = [t.data_ptr() + s for t in tensors for s in starts]
     to, dst = layout, src
@@ -637,4 +637,4 @@ def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=N
                                   None if dst is src else ctypes.byref(to), parents.data_ptr(), B, beams,
                                   _stream(None))
     _check(st, "fs_beam_reorder")
-    return targets[0] if single else targets
+    return written
