@@ -59,7 +59,7 @@ fs_status_t fs_rms_norm_i8(const void* X, int64_t ldx, const void* residual, int
  * one rounding to out_dtype.
  *   Q: int8 [M, K], stride ldq; W: int8 [N, K], stride ldw. Both 16-byte
  *     aligned; K, ldq, ldw multiples of 16; K <= 131056 (no sum of products
- *     of 8-bit values can overflow).
+ *     of 8-bit values can overflow); ldq, ldw < 2^24.
  *   out: [M, N] in out_dtype (bf16 or fp32), stride ldo >= N, any alignment of
  *     the element type. */
 fs_status_t fs_matmul_i8(const int8_t* Q, int64_t ldq, const float* q_scales, const int8_t* W, int64_t ldw,

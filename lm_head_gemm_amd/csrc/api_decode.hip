@@ -13,6 +13,7 @@ constexpr int64_t kMaxRows = 0x7FFFFFFF;
 constexpr int64_t kMaxV = 0x7FFFFFFF;          // tokens are int32
 constexpr int64_t kMaxRowBytes = 159 * 1024;   // a row held in registers by one workgroup
 constexpr int64_t kMaxK = 131056;              // 2^31 / 2^14 - 1, a multiple of 16: no int32 sum overflows
+constexpr int64_t kMaxLd = 1 << 24;            // row offsets within a tile of 256 rows fit 32 bits
 constexpr int64_t kMaxGroups = 65536;
 constexpr size_t kAlign = 256;
 constexpr int32_t kSamplePart = 2048;          // smallest part of a row per sampler workgroup
@@ -41,7 +42,7 @@ fs_status_t check_product(const int8_t* Q, int64_t ldq, const float* q_scales, c
                           const float* w_scales, int64_t M, int64_t N, int64_t K) {
   if (!Q || !q_scales || !W || !w_scales) return FS_ERR_INVALID_ARGUMENT;
   if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || N > kMaxV || ldq < K || ldw < K) return FS_ERR_INVALID_ARGUMENT;
-  if (K > kMaxK || K % 16 || ldq % 16 || ldw % 16) return FS_ERR_UNSUPPORTED;
+  if (K > kMaxK || K % 16 || ldq % 16 || ldw % 16 || ldq >= kMaxLd || ldw >= kMaxLd) return FS_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(W, 16) || !aligned(q_scales, 4) || !aligned(w_scales, 4)) return FS_ERR_UNSUPPORTED;
   return FS_OK;
 }

@@ -10,10 +10,10 @@
 //  * merge: a workgroup per group of beams joins the chunks' sums to the rows'
 //    logarithms in fp64, scores the chunks' entries, and picks the n best.
 //
-// Both pick n of many the same way: split the threads into at least n sets,
-// take each set's largest value, and let t be the smallest of those. At least
-// n values reach t, and usually few more do (about n ln n in random order):
-// these go to LDS, where each counts the ones ahead of it. If too many reach t
+// Both pick n of many the same way: split the values into at least n sets,
+// take each set's largest, and let t be the smallest of those. At least n
+// values reach t, and usually few more do (about n ln n in random order): these
+// go to LDS, where each counts the ones ahead of it. If too many reach t
 // (long runs of equal values), the scan finds the n-th key bit by bit and the
 // merge takes the best one n times.
 #include "fs_decode.h"
@@ -72,6 +72,11 @@ __device__ __forceinline__ void load_piece(const void* row, int v, int V, float 
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ uint64_t order_of(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
 template <typename T>
@@ -223,7 +228,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   constexpr int kMW = kMergeThreads / 64;
   __shared__ double row_score[FS_BEAM_MAX], row_max[FS_BEAM_MAX], row_log[FS_BEAM_MAX];
   __shared__ int row_state[FS_BEAM_MAX];   // 0: not in use, 1: continued, 2: finished
-  __shared__ double red[kMergeThreads];
+  __shared__ uint64_t set_best[FS_BEAM_MAX];
   __shared__ double list_score[kMergeListed];
   __shared__ int64_t list_place[kMergeListed];
   __shared__ int listed;
@@ -255,56 +260,59 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     }
     if (lane == 0) {
       row_state[k] = state;
-      row_score[k] = (double)score;
+      row_score[k] = (double)score + 0.0;   // -0 is 0
       row_max[k] = m;
       row_log[k] = state == 1 ? log(s) : 0.0;
     }
   }
   if (tid == 0) listed = 0;
+  if (tid < FS_BEAM_MAX) set_best[tid] = 0ull;
   __syncthreads();
 
   // entry j of the group: the chunks' entries row by row, then the finished beams
   const int per_row = nc * n;
-  const int64_t total = (int64_t)K * per_row + K;
-  auto entry = [&](int64_t j, Scored* e) -> bool {
-    if (j < (int64_t)K * per_row) {
+  const int64_t scanned = (int64_t)K * per_row, total = scanned + K;
+  const uint64_t* cand = a.cand + (int64_t)b * scanned;
+  auto scored = [&](int64_t j, uint64_t key, Scored* e) -> bool {
+    if (j < scanned) {
       const int k = (int)(j / per_row);
-      if (row_state[k] != 1) return false;
-      const uint64_t key = a.cand[(int64_t)b * K * per_row + j];
-      if (key == 0ull) return false;
+      if (row_state[k] != 1 || key == 0ull) return false;
       const uint32_t o = (uint32_t)(key >> 32);
       const double x = (double)__uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
       e->score = row_score[k] + ((x - row_max[k]) - row_log[k]);
       e->place = (int64_t)k * a.V + key_to_token(key);
       return true;
     }
-    const int k = (int)(j - (int64_t)K * per_row);
+    const int k = (int)(j - scanned);
     if (row_state[k] != 2) return false;
     e->score = row_score[k];
     e->place = (int64_t)k * a.V + a.pad;
     return true;
   };
+  auto entry = [&](int64_t j, Scored* e) -> bool { return scored(j, j < scanned ? cand[j] : 0ull, e); };
 
-  double best = -kInf;
-  for (int64_t j = tid; j < total; j += kMergeThreads) {
+  // The bound, from the first `ranks` entries of every chunk (about eight per
+  // set at least): sets by a multiplicative hash, so that neither the rank nor
+  // the beam of an entry decides its set.
+  int log_s = 2;
+  while ((1 << log_s) < n) ++log_s;
+  const int S = 1 << log_s;
+  const int64_t lists = (int64_t)K * nc;
+  const int ranks = (int)min((int64_t)n, (8 * S + lists - 1) / lists);
+  for (int64_t j = tid; j < lists * ranks; j += kMergeThreads) {
+    const int64_t l = j / ranks;
     Scored e;
-    if (entry(j, &e)) best = fmax(best, e.score);
+    if (entry(l * n + (j - l * ranks), &e))
+      atomicMax(reinterpret_cast<unsigned long long*>(&set_best[((uint32_t)j * 2654435769u) >> (32 - log_s)]),
+                (unsigned long long)order_of(e.score));
   }
-  // sets of threads: tid mod S
-  int S = 4;
-  while (S < n) S *= 2;
-  for (int d = 32; d >= S; d >>= 1) best = fmax(best, __shfl_xor(best, d));
-  red[tid] = best;
   __syncthreads();
-  best = red[lane];
-  for (int w = 1; w < kMW; ++w) best = fmax(best, red[w * 64 + lane]);
-  double bound = best;
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) bound = fmin(bound, __shfl_xor(bound, d));
+  uint64_t bound = ~0ull;
+  for (int i = 0; i < S; ++i) bound = min(bound, set_best[i]);   // 0: a set without entry
 
   for (int64_t j = tid; j < total; j += kMergeThreads) {
     Scored e;
-    if (entry(j, &e) && e.score >= bound) {
+    if (entry(j, &e) && order_of(e.score) >= bound) {
       const int k = atomicAdd(&listed, 1);
       if (k < kMergeListed) {
         list_score[k] = e.score;

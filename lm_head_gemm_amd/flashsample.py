@@ -158,6 +158,12 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+# The current stream's handle of a device, without the Python object around it
+# (2.7 us per call); torch builds without the function take the long way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _check(st: int, where: str):
     if st != FS_OK:
         raise FlashSampleError(st, where)
@@ -350,6 +356,9 @@ def probe_read(src: torch.Tensor, chunk_bytes: int = 1 << 19, sink: torch.Tensor
 
 
 # ------------------------------------------------------- 8-bit head, beam search
+_NOWHERE_ELSE = contextlib.nullcontext()
+
+
 def _on(device: torch.device, stream):
     """Where a call on tensors of `device` allocates and launches: on `stream`
     (a torch stream of that device), or on that device's current stream. What
@@ -361,24 +370,26 @@ def _on(device: torch.device, stream):
         return torch.cuda.stream(stream)
     if device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _NOWHERE_ELSE
 
 
 def _same_device(x: torch.Tensor, *others) -> torch.device:
-    if not x.is_cuda:
+    at = x.get_device()
+    if at < 0:
         raise ValueError("device tensors expected")
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"tensors on one device expected, got {x.device} and {t.device}")
     return x.device
 
 
 def _expect(t: torch.Tensor, shape, dtype, what: str, rows: bool = True):
     """A tensor of this shape and dtype; contiguous rows (2-D) or elements."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    if (t.dim() == 2 and rows and t.shape[1] > 1 and t.stride(1) != 1) or \
-            ((t.dim() == 1 or not rows) and not t.is_contiguous()):
+    if t.is_contiguous():
+        return
+    if not rows or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: contiguous {'rows' if t.dim() == 2 and rows else 'elements'} expected")
 
 
@@ -415,10 +426,11 @@ def quantize_i8(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Te
     loaded) and hidden states that are normed already."""
     M, D = _rows(x)
     dt = _dtype_code(x.dtype)
-    with _on(_same_device(x, q, scales), stream):
+    device = _same_device(x, q, scales)
+    with _on(device, stream):
         q, scales = _codes(x, q, scales)
         st = _lib.fs_quantize_i8(x.data_ptr(), _ld(x), dt, M, D, q.data_ptr(), _ld(q), scales.data_ptr(),
-                                 _stream(None))
+                                 _raw_stream(device.index))
     _check(st, "fs_quantize_i8")
     return q, scales
 
@@ -438,7 +450,8 @@ def rms_norm_i8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual
         _expect(residual, (M, D), x.dtype, "residual")
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
-    with _on(_same_device(x, gain, residual, sum_out, q, scales), stream):
+    device = _same_device(x, gain, residual, sum_out, q, scales)
+    with _on(device, stream):
         if residual is not None:
             if sum_out is None:
                 sum_out = torch.empty((M, D), dtype=x.dtype, device=x.device)
@@ -449,7 +462,7 @@ def rms_norm_i8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual
                                  0 if residual is None else _ld(residual), gain.data_ptr(), gt, dt, M, D, float(eps),
                                  None if residual is None else sum_out.data_ptr(),
                                  0 if residual is None else _ld(sum_out), q.data_ptr(), _ld(q), scales.data_ptr(),
-                                 _stream(None))
+                                 _raw_stream(device.index))
     _check(st, "fs_rms_norm_i8")
     return (q, scales) if residual is None else (q, scales, sum_out)
 
@@ -470,7 +483,8 @@ def matmul_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     [M, K] and w [N, K], summed exactly in integers (fs_matmul_i8): [M, N] in
     out's dtype, or out_dtype (bf16 or fp32). K is a multiple of 16."""
     M, N, K = _product_inputs(q, q_scales, w, w_scales)
-    with _on(_same_device(q, q_scales, w, w_scales, out), stream):
+    device = _same_device(q, q_scales, w, w_scales, out)
+    with _on(device, stream):
         if out is None:
             dt = _dtype_code(out_dtype)
             out = torch.empty((M, N), dtype=out_dtype, device=q.device)
@@ -478,7 +492,7 @@ def matmul_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
             _expect(out, (M, N), out.dtype, "out")
             dt = _dtype_code(out.dtype)
         st = _lib.fs_matmul_i8(q.data_ptr(), _ld(q), q_scales.data_ptr(), w.data_ptr(), _ld(w), w_scales.data_ptr(),
-                               M, N, K, out.data_ptr(), _ld(out), dt, _stream(None))
+                               M, N, K, out.data_ptr(), _ld(out), dt, _raw_stream(device.index))
     _check(st, "fs_matmul_i8")
     return out
 
@@ -494,7 +508,8 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     codes q [B, D] and an 8-bit LM head w [V, D] (fs_sample_i8). Noise, ties
     and NaN rule are sample_fused's."""
     B, V, D = _product_inputs(q, q_scales, w, w_scales)
-    with _on(_same_device(q, q_scales, w, w_scales, out, workspace), stream):
+    device = _same_device(q, q_scales, w, w_scales, out, workspace)
+    with _on(device, stream):
         if out is None:
             out = torch.empty(B, dtype=torch.int32, device=q.device)
         else:
@@ -503,7 +518,7 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
             workspace = torch.empty(max(sample_i8_workspace_bytes(B, D, V), 256), dtype=torch.uint8, device=q.device)
         st = _lib.fs_sample_i8(q.data_ptr(), _ld(q), q_scales.data_ptr(), w.data_ptr(), _ld(w), w_scales.data_ptr(),
                                B, D, V, float(temperature), int(seed), int(step), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), out.data_ptr(), _stream(None))
+                               workspace.numel() * workspace.element_size(), out.data_ptr(), _raw_stream(device.index))
     _check(st, "fs_sample_i8")
     return out
 
@@ -536,7 +551,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
             raise ValueError(f"finished: bool or uint8 expected, got {finished.dtype}")
         _expect(finished, (B, beams), finished.dtype, "finished", rows=False)
     given = out if out is not None else ()
-    with _on(_same_device(logits, scores, finished, workspace, *given), stream):
+    device = _same_device(logits, scores, finished, workspace, *given)
+    with _on(device, stream):
         if out is None:
             out = (torch.empty((B, n), dtype=torch.float32, device=logits.device),
                    torch.empty((B, n), dtype=torch.int32, device=logits.device),
@@ -551,7 +567,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
         st = _lib.fs_beam_select(logits.data_ptr(), _ld(logits), dt, scores.data_ptr(),
                                  None if finished is None else finished.data_ptr(), int(pad_token), B, beams, V, n,
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _stream(None))
+                                 out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _raw_stream(device.index))
     _check(st, "fs_beam_select")
     return tuple(out)
 
@@ -635,6 +651,6 @@ def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=N
     with _on(device, stream):
         st = _lib.fs_beam_reorder(table(*src), None if dst is src else table(*dst), len(src), ctypes.byref(layout),
                                   None if dst is src else ctypes.byref(to), parents.data_ptr(), B, beams,
-                                  _stream(None))
+                                  _raw_stream(device.index))
     _check(st, "fs_beam_reorder")
     return written

@@ -43,8 +43,9 @@ def rms_norm(x: np.ndarray, gain: np.ndarray, eps: float, residual=None, bf16=Fa
 
 
 def product(q: np.ndarray, q_scales: np.ndarray, w: np.ndarray, w_scales: np.ndarray) -> np.ndarray:
-    """fp32 logits of 8-bit codes: whole-number sums, then two fp32 products."""
-    sums = q.astype(np.int64) @ w.astype(np.int64).T
+    """fp32 logits of 8-bit codes: whole-number sums, then two fp32 products.
+    (The sums stay below 2^53, so fp64 holds every one of them exactly.)"""
+    sums = q.astype(np.float64) @ w.astype(np.float64).T
     return (sums.astype(np.float32) * q_scales.astype(np.float32)[:, None]) * w_scales.astype(np.float32)[None, :]
 
 

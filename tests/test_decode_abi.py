@@ -62,6 +62,7 @@ PRODUCT = dict(Q=FAKE, ldq=64, qs=FAKE, W=FAKE, ldw=64, ws=FAKE, M=4, N=100, K=6
     (dict(N=2**31), INVALID), (dict(M=2**31), INVALID), (dict(ldq=48), INVALID), (dict(ldw=48), INVALID),
     (dict(ldo=99), INVALID), (dict(K=56), UNSUPPORTED), (dict(ldq=72), UNSUPPORTED), (dict(ldw=72), UNSUPPORTED),
     (dict(K=131072, ldq=131072, ldw=131072), UNSUPPORTED), (dict(Q=FAKE + 8), UNSUPPORTED),
+    (dict(ldq=2**24), UNSUPPORTED), (dict(ldw=2**24), UNSUPPORTED),
     (dict(W=FAKE + 4), UNSUPPORTED), (dict(qs=FAKE + 1), UNSUPPORTED), (dict(ws=FAKE + 2), UNSUPPORTED),
     (dict(out=FAKE + 1), UNSUPPORTED), (dict(out=FAKE + 2, dtype=F32), UNSUPPORTED), (dict(dtype=9), UNSUPPORTED),
 ])
