@@ -14,12 +14,10 @@
 //    BKB contiguous bytes. Which 16-byte piece of its row a lane fetches is
 //    chosen so that the operand reads (ds_read_b128: 16 rows, one K step) meet
 //    no bank twice: piece p of row r lies at p ^ swizzle(r).
-//  * Each K step's operands are read while the matrix instructions of the step
-//    before run. Between the reads of a stage's last step and its matrix
-//    instructions each wave waits for its own copies of the next stage (later
-//    ones stay in flight), one workgroup barrier, the copies of stage s + NS are
-//    issued into the buffer that stage s has left, and the next stage's first
-//    operands are read.
+//  * Per stage: each wave waits for its own copies of it (later ones stay in
+//    flight), one workgroup barrier, all operand reads of stage s, the copies of
+//    stage s + NS - 1 into the buffer that stage s - 1 has left, and the matrix
+//    instructions.
 //  * K need not be a multiple of BKB: for pieces past K the stage's first one is
 //    fetched, and Q's are zeroed in LDS by the wave that fetched them.
 //    Whatever W holds there counts nothing, the products being integers.
@@ -74,7 +72,6 @@ __global__ __launch_bounds__(64 * NWW * NWT) void product_i8_kernel(ProductI8Arg
   constexpr int WRC = WR % 2 == 0 ? 2 : 1;                // epilogue: blocks of channels at a time
   constexpr int ROW = 16 * WRC + 4;                       // padded row of one token, floats
   static_assert((BM + BN) % (RPL * NW) == 0 && BM % RPL == 0, "even shares of the copies");
-  static_assert(KS % 2 == 0, "a stage's first operands go to set 0");
   static_assert(NW * 16 * ROW * 4 <= NS * STAGE, "the epilogue's tiles fit the ring");
   __shared__ __align__(1024) unsigned char ring[NS * STAGE];
 
@@ -135,23 +132,26 @@ __global__ __launch_bounds__(64 * NWW * NWT) void product_i8_kernel(ProductI8Arg
 #pragma unroll
   for (int t = 0; t < KS; ++t) k_at[t] = 16 * ((4 * t + q) ^ swizzle(r));
 
-  // Operands of one K step; two sets, so that a step's reads are in flight
-  // under the matrix instructions of the step before.
-  i32x4 av[2][WR], bv[2][TC];
+  i32x4 av[KS][WR], bv[KS][TC];
   i32x4 acc[WR][TC];
-  auto read = [&](int buf, int t, int set) {
-    const unsigned char* st = ring + buf * STAGE + k_at[t];
+  auto read = [&](int buf) {   // the whole stage's operands, so that one wait serves all K steps
+    const unsigned char* st = ring + buf * STAGE;
 #pragma unroll
-    for (int j = 0; j < WR; ++j) av[set][j] = *reinterpret_cast<const i32x4*>(st + a_at + j * 16 * BKB);
+    for (int t = 0; t < KS; ++t) {
 #pragma unroll
-    for (int c = 0; c < TC; ++c) bv[set][c] = *reinterpret_cast<const i32x4*>(st + b_at + c * 16 * BKB);
+      for (int j = 0; j < WR; ++j) av[t][j] = *reinterpret_cast<const i32x4*>(st + k_at[t] + a_at + j * 16 * BKB);
+#pragma unroll
+      for (int c = 0; c < TC; ++c) bv[t][c] = *reinterpret_cast<const i32x4*>(st + k_at[t] + b_at + c * 16 * BKB);
+    }
   };
-  auto multiply = [&](int set) {
+  auto multiply = [&]() {
 #pragma unroll
-    for (int c = 0; c < TC; ++c)
+    for (int t = 0; t < KS; ++t)
 #pragma unroll
-      for (int j = 0; j < WR; ++j)
-        acc[j][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[set][j], bv[set][c], acc[j][c], 0, 0, 0);
+      for (int c = 0; c < TC; ++c)
+#pragma unroll
+        for (int j = 0; j < WR; ++j)
+          acc[j][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[t][j], bv[t][c], acc[j][c], 0, 0, 0);
   };
   const int partial = a.K % BKB == 0 ? -1 : S - 1 - s0;   // the partial stage's turn
   // Stage s, in `buf`, is complete in LDS and everyone's reads of earlier ones
@@ -161,38 +161,21 @@ __global__ __launch_bounds__(64 * NWW * NWT) void product_i8_kernel(ProductI8Arg
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       zero_tail(buf);
     }
-    __builtin_amdgcn_sched_barrier(0);
     wait_copies_and_sync<decltype(left_c)::value>();
-    __builtin_amdgcn_sched_barrier(0);
   };
-  using First = std::integral_constant<int, (NS - 1) * LPW>;
-  using Later = std::integral_constant<int, (NS - 2) * LPW>;
-  using None = std::integral_constant<int, 0>;
-
 #pragma unroll
   for (int j = 0; j < WR; ++j)
 #pragma unroll
     for (int c = 0; c < TC; ++c) acc[j][c] = i32x4{0, 0, 0, 0};
-  for (int s = 0; s < NS && s < S; ++s) issue(s, s);
-  if (S >= NS) arrive(0, 0, First{});
-  else arrive(0, 0, None{});
-  read(0, 0, 0);
+  for (int s = 0; s < NS - 1 && s < S; ++s) issue(s, s);
   int buf = 0;
   for (int s = 0; s < S; ++s) {
-    const int next = buf == NS - 1 ? 0 : buf + 1;
-#pragma unroll
-    for (int t = 0; t < KS - 1; ++t) {
-      read(buf, t + 1, (t + 1) & 1);
-      multiply(t & 1);
-    }
-    if (s + 1 < S) {
-      if (s + NS <= S) arrive(s + 1, next, Later{});
-      else arrive(s + 1, next, None{});
-      if (s + NS < S) issue(s + NS, buf);
-      read(next, 0, 0);
-    }
-    multiply((KS - 1) & 1);
-    buf = next;
+    if (s + NS - 1 <= S) arrive(s, buf, std::integral_constant<int, (NS - 2) * LPW>{});
+    else arrive(s, buf, std::integral_constant<int, 0>{});
+    read(buf);
+    if (s + NS - 1 < S) issue(s + NS - 1, buf == 0 ? NS - 1 : buf - 1);
+    multiply();
+    buf = buf == NS - 1 ? 0 : buf + 1;
   }
 
   // A lane holds four neighbouring channels of one token; through a wave's own
@@ -265,6 +248,71 @@ __global__ __launch_bounds__(64 * NWW * NWT) void product_i8_kernel(ProductI8Arg
   else write(std::false_type{});
 }
 
+// Few, small tiles: 16 channels x 16 TC tokens per workgroup, whose 8 waves
+// share out the K steps (wave w takes steps w, w + 8, ...), straight from memory
+// to registers, and add their whole-number sums in LDS. A tile of the kernel
+// above spends about 0.55 us on each 256 bytes of K, whatever is in flight
+// (its barrier and its waves' instructions, one wave per SIMD); here a wave has
+// four K steps in flight at once and no barrier before the end.
+template <int TC>
+__global__ __launch_bounds__(512) void product_i8_small_kernel(ProductI8Args a, int n_wt) {
+  constexpr int NW = 8, U = 4, ROW = 17;
+  __shared__ int32_t sums[NW][16 * TC][ROW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  const int vt = blockIdx.x % n_wt, mt = blockIdx.x / n_wt;
+  const int n0 = vt * 16, m0 = mt * 16 * TC;
+  const int8_t* w = a.w + (int64_t)min(n0 + r, a.N - 1) * a.ldw;
+  const int8_t* x[TC];
+  i32x4 acc[TC];
+#pragma unroll
+  for (int c = 0; c < TC; ++c) {
+    x[c] = a.q + (int64_t)min(m0 + 16 * c + r, a.M - 1) * a.ldq;
+    acc[c] = i32x4{0, 0, 0, 0};
+  }
+  for (int k0 = 64 * wave; k0 < a.K; k0 += 64 * NW * U) {
+    i32x4 av[U], bv[U][TC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 64 * NW * u + 16 * q;
+      av[u] = i32x4{0, 0, 0, 0};
+      if (k < a.K) av[u] = *reinterpret_cast<const i32x4*>(w + k);
+#pragma unroll
+      for (int c = 0; c < TC; ++c) {
+        bv[u][c] = i32x4{0, 0, 0, 0};
+        if (k < a.K) bv[u][c] = *reinterpret_cast<const i32x4*>(x[c] + k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < TC; ++c) acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[u], bv[u][c], acc[c], 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < TC; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[wave][16 * c + r][4 * q + e] = acc[c][e];
+  __syncthreads();
+  for (int i = tid; i < 256 * TC; i += 64 * NW) {
+    const int m = m0 + i / 16, n = n0 + i % 16;
+    if (m >= a.M || n >= a.N) continue;
+    int32_t sum = 0;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) sum += sums[v][i / 16][i % 16];
+    const float y = ((float)sum * a.q_scales[m]) * a.w_scales[n];
+    const int64_t at = (int64_t)m * a.ldo + n;
+    if (a.out_bf16) static_cast<uint16_t*>(a.out)[at] = f32_to_bf16_rne(y);
+    else static_cast<float*>(a.out)[at] = y;
+  }
+}
+
+template <int TC>
+hipError_t go_small(const ProductI8Args& a, hipStream_t stream) {
+  const int64_t n_wt = ((int64_t)a.N + 15) / 16, n_mt = ((int64_t)a.M + 16 * TC - 1) / (16 * TC);
+  if (!grid_fits(n_wt * n_mt, 512)) return hipErrorInvalidConfiguration;
+  return launch(product_i8_small_kernel<TC>, dim3((unsigned)(n_wt * n_mt)), dim3(512), 0, stream, a, (int)n_wt);
+}
+
 template <int WR, int TC, int NWW, int NWT, int BKB, int NS, bool ONE>
 hipError_t go(const ProductI8Args& a, hipStream_t stream) {
   constexpr int BM = 16 * WR * NWW, BN = 16 * TC * NWT;
@@ -278,21 +326,36 @@ hipError_t go(const ProductI8Args& a, hipStream_t stream) {
 
 }  // namespace
 
-#ifndef PRODUCT_PROBE
+// The tile by the number of tiles it leaves. A launch wants most of the 256 CUs
+// busy; beyond that, larger tiles move fewer bytes per product. Measured (us,
+// M x N x K; the tile taken first, channels x tokens):
+//   M <= 16: 64 x 16 from N = 16384 on (16 x 16384 x 4096: 12.4, small 15.8;
+//     1 x 128256 x 4096: 80), else the small kernel (1 x 5003 x 4096: 7.6, 11.5)
+//   M <= 32: 128 x 32 (32 x 128256 x 4096: 83, with 128 x 64 tiles 88)
+//   64 x 152064 x 3584: 128 x 64 100, 256 x 64 116, 64 x 64 123
+//   128 x 128256 x 4096: 256 x 128 118, 128 x 128 134
+//   1024 x 16384 x 4096: 256 x 256 75, 128 x 128 81; 1024 x 5003 x 2320:
+//     128 x 128 27, 256 x 256 47; 300 x 5003 x 512: 128 x 64 7.3, 128 x 128 9.1,
+//     32 x 64 9.7; 128 x 5003 x 4096: 32 x 64 14.8, 128 x 64 22.8, small 29.7
+//   45 x 5003 x 2320: small 8.5, 32 x 64 9.7
+// Rings of three or four stages and two workgroups per CU (one for the two
+// largest tiles, whose LDS holds no more): deeper rings with one workgroup
+// measured 5-15% slower on the memory-bound shapes, stages of half the length
+// 5-25% slower.
 hipError_t launch_product_i8(const ProductI8Args& a, hipStream_t stream) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((a.N + bm - 1) / bm) * ((a.M + bn - 1) / bn); };
-  if (a.M <= 16) return tiles(64, 16) < 256 ? go<1, 1, 2, 1, 256, 4, true>(a, stream) : go<1, 1, 4, 1, 256, 3, true>(a, stream);
-  if (a.M <= 32 && tiles(128, 32) >= 256) return go<2, 2, 4, 1, 256, 2, true>(a, stream);
-  if (a.M <= 64 && tiles(128, 64) >= 256) {
-    const int64_t last = tiles(256, 64) % 512;
-    if (last == 0 || last >= 288) return go<4, 2, 4, 2, 128, 2, true>(a, stream);
-    return go<2, 2, 4, 2, 128, 3, true>(a, stream);
+  if (a.M <= 16) {
+    if (tiles(64, 16) >= 256) return go<1, 1, 4, 1, 256, 4, true>(a, stream);
+    return go_small<1>(a, stream);
   }
-  if (a.M <= 128 && tiles(256, 128) >= 192) return go<4, 4, 4, 2, 128, 3, true>(a, stream);
+  if (a.M <= 32 && tiles(128, 32) >= 192) return go<2, 2, 4, 1, 128, 4, true>(a, stream);
   if (a.M > 128 && tiles(256, 256) >= 192) return go<4, 8, 4, 2, 128, 2, false>(a, stream);
+  if (a.M > 64 && a.M <= 128 && tiles(256, 128) >= 192) return go<4, 4, 4, 2, 128, 3, true>(a, stream);
   if (a.M > 64 && tiles(128, 128) >= 192) return go<2, 4, 4, 2, 128, 2, false>(a, stream);
-  return go<1, 4, 4, 1, 128, 3, false>(a, stream);
+  if (tiles(128, 64) >= 192)
+    return a.M <= 64 ? go<2, 2, 4, 2, 128, 3, true>(a, stream) : go<2, 2, 4, 2, 128, 3, false>(a, stream);
+  if (tiles(32, 64) >= 256) return go<1, 2, 2, 2, 256, 3, false>(a, stream);
+  return go_small<4>(a, stream);
 }
-#endif
 
 }  // namespace fs
