@@ -93,7 +93,7 @@ fs_status_t fs_sample_i8(const int8_t* Q, int64_t ldq, const float* q_scales, co
  * leaves its beam without continuation. Where fewer than n continuations
  * exist the rest of the outputs are -inf, -1, -1. */
 #define FS_BEAM_MAX 64
-size_t fs_beam_select_workspace_bytes(int64_t B, int64_t beams, int64_t V, int64_t n);
+size_t fs_beam_select_workspace_bytes(int64_t B, int64_t beams, int64_t V, int64_t n, fs_dtype_t logits_dtype);
 fs_status_t fs_beam_select(const void* logits, int64_t ld_logits, fs_dtype_t logits_dtype, const float* scores,
                            const uint8_t* finished, int32_t pad_token, int64_t B, int64_t beams, int64_t V, int64_t n,
                            void* workspace, size_t workspace_bytes, float* out_scores, int32_t* out_parents,

@@ -88,10 +88,10 @@ struct SelectSpace {
   int64_t chunks;
   size_t sums, maxima, bytes;   // offsets behind the keys, and the end
 };
-SelectSpace select_space(int64_t B, int64_t beams, int64_t V, int64_t n) {
+SelectSpace select_space(int64_t B, int64_t beams, int64_t V, int64_t n, bool bf16) {
   SelectSpace s;
   const int64_t rows = B * beams;
-  s.chunk = beam_chunk(rows, V);
+  s.chunk = beam_chunk(rows, V, bf16);
   s.chunks = (V + s.chunk - 1) / s.chunk;
   s.sums = align_up((size_t)(rows * s.chunks * n) * sizeof(uint64_t));
   s.maxima = s.sums + align_up((size_t)(rows * s.chunks) * sizeof(double));
@@ -243,8 +243,9 @@ fs_status_t fs_sample_i8(const int8_t* Q, int64_t ldq, const float* q_scales, co
   return run(launch_stage2(partial, (int32_t)B, n_parts, out_tokens, stream));
 }
 
-size_t fs_beam_select_workspace_bytes(int64_t B, int64_t beams, int64_t V, int64_t n) {
-  return select_sizes_ok(B, beams, V, n) ? select_space(B, beams, V, n).bytes : 0;
+size_t fs_beam_select_workspace_bytes(int64_t B, int64_t beams, int64_t V, int64_t n, fs_dtype_t logits_dtype) {
+  if (!select_sizes_ok(B, beams, V, n) || !dtype_ok(logits_dtype)) return 0;
+  return select_space(B, beams, V, n, logits_dtype == FS_DTYPE_BF16).bytes;
 }
 
 fs_status_t fs_beam_select(const void* logits, int64_t ld_logits, fs_dtype_t logits_dtype, const float* scores,
@@ -258,7 +259,7 @@ fs_status_t fs_beam_select(const void* logits, int64_t ld_logits, fs_dtype_t log
   if (!aligned(workspace, 16) || !aligned(scores, 4) || !aligned(out_scores, 4) || !aligned(out_parents, 4) ||
       !aligned(out_tokens, 4))
     return FS_ERR_UNSUPPORTED;
-  const SelectSpace s = select_space(B, beams, V, n);
+  const SelectSpace s = select_space(B, beams, V, n, logits_dtype == FS_DTYPE_BF16);
   if (workspace_bytes < s.bytes) return FS_ERR_WORKSPACE_TOO_SMALL;
   BeamSelectArgs a{};
   a.logits = logits;

@@ -67,7 +67,7 @@ struct BeamReorderArgs {
 hipError_t launch_rows_i8(const RowsI8Args& a, bool bf16, bool gain_bf16, hipStream_t stream);
 hipError_t launch_product_i8(const ProductI8Args& a, hipStream_t stream);
 // Vocabulary entries per chunk of the selection's first kernel.
-int32_t beam_chunk(int64_t rows, int64_t V);
+int32_t beam_chunk(int64_t rows, int64_t V, bool bf16);
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t stream);
 hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t stream);
 

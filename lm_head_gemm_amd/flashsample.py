@@ -131,7 +131,7 @@ def _load():
     lib.fs_sample_i8.restype = ctypes.c_int
     lib.fs_sample_i8.argtypes = product + [ctypes.c_float, c_u64, c_u64, vp, c_sz, vp, vp]
     lib.fs_beam_select_workspace_bytes.restype = c_sz
-    lib.fs_beam_select_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64]
+    lib.fs_beam_select_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64, ctypes.c_int]
     lib.fs_beam_select.restype = ctypes.c_int
     lib.fs_beam_select.argtypes = [vp, c_i64, ctypes.c_int, vp, vp, ctypes.c_int32, c_i64, c_i64, c_i64, c_i64,
                                    vp, c_sz, vp, vp, vp, vp]
@@ -523,8 +523,8 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     return out
 
 
-def beam_select_workspace_bytes(B, beams, V, n) -> int:
-    return int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n))
+def beam_select_workspace_bytes(B, beams, V, n, dtype=torch.bfloat16) -> int:
+    return int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n, _dtype_code(dtype)))
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None,
@@ -562,7 +562,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
                                       ("out scores", "out parents", "out tokens"), strict=True):
                 _expect(t, (B, n), dtype, what, rows=False)
         if workspace is None:
-            nbytes = beam_select_workspace_bytes(B, beams, V, n)
+            nbytes = int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n, dt))
             workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=logits.device)
         st = _lib.fs_beam_select(logits.data_ptr(), _ld(logits), dt, scores.data_ptr(),
                                  None if finished is None else finished.data_ptr(), int(pad_token), B, beams, V, n,

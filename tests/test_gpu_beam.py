@@ -57,7 +57,8 @@ def _check(fs, logits, scores, n, bf16=False, finished=None, pad=0, least=0.8, g
 @pytest.mark.parametrize("B,K,V,n", [
     (1, 1, 1, 1), (1, 1, 5, 8), (2, 3, 7, 4), (1, 4, 100, 8), (3, 5, 2047, 5), (2, 4, 2048, 8), (2, 4, 2049, 16),
     (5, 2, 5003, 3), (1, 12, 16385, 24), (1, 4, 50257, 8), (4, 8, 33000, 16), (1, 64, 3001, 64), (2, 33, 1000, 33),
-    (40, 4, 4099, 8), (1, 2, 151936, 64), (300, 2, 300, 4), (64, 5, 9001, 10)])
+    (40, 4, 4099, 8), (1, 2, 151936, 64), (300, 2, 300, 4), (64, 5, 9001, 10),
+    (30, 8, 33003, 16), (64, 8, 40001, 8), (1, 64, 20011, 64)])
 def test_selection(fs, bf16, B, K, V, n):
     rng = np.random.default_rng(B * 100 + K * 10 + V + n)
     logits = rng.standard_normal((B * K, V)) * 2
@@ -164,7 +165,7 @@ def test_strided_logits_and_given_outputs(fs):
             wide[:, off:off + V] = _t(logits, dtype)
             out = (torch.zeros((B, n), device="cuda"), torch.zeros((B, n), dtype=torch.int32, device="cuda"),
                    torch.zeros((B, n), dtype=torch.int32, device="cuda"))
-            work = torch.empty(fs.beam_select_workspace_bytes(B, K, V, n), dtype=torch.uint8, device="cuda")
+            work = torch.empty(fs.beam_select_workspace_bytes(B, K, V, n, dtype), dtype=torch.uint8, device="cuda")
             got = fs.beam_select(wide[:, off:off + V], _t(scores), n, out=out, workspace=work)
             assert all(a is b for a, b in zip(got, out))
             assert all(torch.equal(a, b) for a, b in zip(got, want))
