@@ -302,14 +302,13 @@ fs_status_t fs_beam_reorder(const void* const* states, void* const* out, int64_t
   if (!make_levels(to, B * beams, &written) || !make_levels(from, B * beams, &read)) return FS_ERR_INVALID_ARGUMENT;
   const bool alike = from.outer_stride == to.outer_stride && from.row_stride == to.row_stride &&
                      from.block_stride == to.block_stride;
-  BeamReorderArgs a{};
+  void* targets[FS_BEAM_MAX_STATES];
   Buffer all[2 * FS_BEAM_MAX_STATES];
   int n_all = 0;
   for (int64_t i = 0; i < n_states; ++i) {
-    a.src[i] = static_cast<const char*>(states[i]);
-    a.dst[i] = out ? static_cast<char*>(out[i]) : const_cast<char*>(a.src[i]);
-    all[n_all++] = Buffer{(int64_t)(intptr_t)a.dst[i], true};
-    if (out) all[n_all++] = Buffer{(int64_t)(intptr_t)a.src[i], false};
+    targets[i] = out ? out[i] : const_cast<void*>(states[i]);
+    all[n_all++] = Buffer{(int64_t)(intptr_t)targets[i], true};
+    if (out) all[n_all++] = Buffer{(int64_t)(intptr_t)states[i], false};
   }
   // pairs of which one is written; in order of address, so that far ones are not looked at
   std::sort(all, all + n_all, [](const Buffer& x, const Buffer& y) { return x.at < y.at; });
@@ -322,6 +321,7 @@ fs_status_t fs_beam_reorder(const void* const* states, void* const* out, int64_t
       const bool meet = same_levels ? share(written, delta) : delta < (all[i].written ? written : read).span[0];
       if (meet) return FS_ERR_INVALID_ARGUMENT;
     }
+  BeamReorderArgs a{};
   a.from = from;
   a.to = to;
   a.parents = parents;
@@ -329,7 +329,7 @@ fs_status_t fs_beam_reorder(const void* const* states, void* const* out, int64_t
   a.B = (int32_t)B;
   a.beams = (int32_t)beams;
   a.in_place = out == nullptr;
-  return run(launch_beam_reorder(a, stream));
+  return run(launch_beam_reorder(a, states, targets, stream));
 }
 
 }  // extern "C"

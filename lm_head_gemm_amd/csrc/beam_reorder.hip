@@ -13,10 +13,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// The buffers of a call, as a kernel argument: short for the few buffers of most
+// calls (a launch copies its arguments twice: 3 KiB cost it about 1 us).
+template <int N>
+struct Buffers {
+  const char* src[N];
+  char* dst[N];
+};
+
 // Unit U, groups of up to KMAX rows.
-template <typename U, int KMAX>
-__global__ __launch_bounds__(kThreads) void beam_reorder_kernel(BeamReorderArgs a, uint32_t units_per_block,
-                                                                uint32_t units, int64_t groups) {
+template <typename U, int KMAX, int N>
+__global__ __launch_bounds__(kThreads) void beam_reorder_kernel(BeamReorderArgs a, Buffers<N> buffers,
+                                                                uint32_t units_per_block, uint32_t units,
+                                                                int64_t groups) {
   const int K = a.beams;
   for (int64_t g = blockIdx.y; g < groups; g += gridDim.y) {
     // g = (state * outer + slab) * B + b
@@ -24,8 +33,8 @@ __global__ __launch_bounds__(kThreads) void beam_reorder_kernel(BeamReorderArgs 
     const int64_t so = g / a.B;
     const int slab = (int)(so % a.from.outer), state = (int)(so / a.from.outer);
     const int32_t* parents = a.parents + (int64_t)b * K;
-    const char* src = a.src[state] + slab * a.from.outer_stride + (int64_t)b * K * a.from.row_stride;
-    char* dst = a.dst[state] + slab * a.to.outer_stride + (int64_t)b * K * a.to.row_stride;
+    const char* src = buffers.src[state] + slab * a.from.outer_stride + (int64_t)b * K * a.from.row_stride;
+    char* dst = buffers.dst[state] + slab * a.to.outer_stride + (int64_t)b * K * a.to.row_stride;
     for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
       const uint32_t blk = u / units_per_block, off = u - blk * units_per_block;
       const char* s = src + (int64_t)blk * a.from.block_stride + (int64_t)off * sizeof(U);
@@ -49,8 +58,8 @@ __global__ __launch_bounds__(kThreads) void beam_reorder_kernel(BeamReorderArgs 
   }
 }
 
-template <typename U, int KMAX>
-hipError_t go(const BeamReorderArgs& a, hipStream_t stream) {
+template <typename U, int KMAX, int N>
+hipError_t go(const BeamReorderArgs& a, const void* const* states, void* const* out, hipStream_t stream) {
   const int64_t per_block = a.from.block_bytes / (int64_t)sizeof(U);
   // a row's units are counted in 31 bits (16-byte units: rows up to 32 GiB)
   if (per_block > 0x7FFFFFFF / a.from.blocks || a.from.outer > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
@@ -59,28 +68,40 @@ hipError_t go(const BeamReorderArgs& a, hipStream_t stream) {
   int64_t gx = (units + kThreads - 1) / kThreads;
   if (gx > 65536) gx = 65536;
   const int64_t gy = groups < 65535 ? groups : 65535;
-  return launch(beam_reorder_kernel<U, KMAX>, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), 0, stream, a,
-                (uint32_t)per_block, (uint32_t)units, groups);
+  Buffers<N> buffers;
+  for (int i = 0; i < a.n_states; ++i) {
+    buffers.src[i] = static_cast<const char*>(states[i]);
+    buffers.dst[i] = static_cast<char*>(out[i]);
+  }
+  return launch(beam_reorder_kernel<U, KMAX, N>, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), 0, stream, a,
+                buffers, (uint32_t)per_block, (uint32_t)units, groups);
+}
+
+template <typename U, int N>
+hipError_t by_beams(const BeamReorderArgs& a, const void* const* states, void* const* out, hipStream_t stream) {
+  if (a.beams <= 4) return go<U, 4, N>(a, states, out, stream);
+  if (a.beams <= 8) return go<U, 8, N>(a, states, out, stream);
+  if (a.beams <= 16) return go<U, 16, N>(a, states, out, stream);
+  return go<U, 64, N>(a, states, out, stream);
 }
 
 template <typename U>
-hipError_t by_beams(const BeamReorderArgs& a, hipStream_t stream) {
-  if (a.beams <= 4) return go<U, 4>(a, stream);
-  if (a.beams <= 8) return go<U, 8>(a, stream);
-  if (a.beams <= 16) return go<U, 16>(a, stream);
-  return go<U, 64>(a, stream);
+hipError_t by_states(const BeamReorderArgs& a, const void* const* states, void* const* out, hipStream_t stream) {
+  return a.n_states <= 8 ? by_beams<U, 8>(a, states, out, stream)
+                         : by_beams<U, FS_BEAM_MAX_STATES>(a, states, out, stream);
 }
 
 }  // namespace
 
-hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t stream) {
+hipError_t launch_beam_reorder(const BeamReorderArgs& a, const void* const* states, void* const* out,
+                               hipStream_t stream) {
   uint64_t bits = (uint64_t)(a.from.outer_stride | a.from.row_stride | a.from.block_stride | a.from.block_bytes |
                              a.to.outer_stride | a.to.row_stride | a.to.block_stride);
-  for (int i = 0; i < a.n_states; ++i) bits |= (uint64_t)(uintptr_t)a.src[i] | (uint64_t)(uintptr_t)a.dst[i];
+  for (int i = 0; i < a.n_states; ++i) bits |= (uint64_t)(uintptr_t)states[i] | (uint64_t)(uintptr_t)out[i];
   // the widest unit that every address and length is a multiple of
-  if (bits % 16 == 0) return by_beams<uint4>(a, stream);
-  if (bits % 4 == 0) return by_beams<uint32_t>(a, stream);
-  return by_beams<uint8_t>(a, stream);
+  if (bits % 16 == 0) return by_states<uint4>(a, states, out, stream);
+  if (bits % 4 == 0) return by_states<uint32_t>(a, states, out, stream);
+  return by_states<uint8_t>(a, states, out, stream);
 }
 
 }  // namespace fs

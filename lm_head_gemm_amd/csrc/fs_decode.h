@@ -56,8 +56,6 @@ struct BeamSelectArgs {
 };
 
 struct BeamReorderArgs {
-  const char* src[FS_BEAM_MAX_STATES];
-  char* dst[FS_BEAM_MAX_STATES];
   fs_beam_layout_t from, to;
   const int32_t* parents;
   int32_t n_states, B, beams;
@@ -69,6 +67,8 @@ hipError_t launch_product_i8(const ProductI8Args& a, hipStream_t stream);
 // Vocabulary entries per chunk of the selection's first kernel.
 int32_t beam_chunk(int64_t rows, int64_t V, bool bf16);
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t stream);
-hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t stream);
+// states, out: host arrays of a.n_states device addresses (in place: the same one twice).
+hipError_t launch_beam_reorder(const BeamReorderArgs& a, const void* const* states, void* const* out,
+                               hipStream_t stream);
 
 }  // namespace fs

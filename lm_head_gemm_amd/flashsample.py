@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch  # loads the HIP runtime the library binds to
@@ -162,6 +163,7 @@ def _stream(stream) -> int:
 # (2.7 us per call); torch builds without the function take the long way.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _check(st: int, where: str):
@@ -368,7 +370,7 @@ def _on(device: torch.device, stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         return torch.cuda.device(device)
     return _NOWHERE_ELSE
 
@@ -383,40 +385,44 @@ def _same_device(x: torch.Tensor, *others) -> torch.device:
     return x.device
 
 
-def _expect(t: torch.Tensor, shape, dtype, what: str, rows: bool = True):
-    """A tensor of this shape and dtype; contiguous rows (2-D) or elements."""
-    if t.shape != shape or t.dtype != dtype:
+def _expect(t: torch.Tensor, shape, dtype, what: str):
+    """A contiguous tensor of this shape and dtype."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{what}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous elements expected")
+
+
+def _rows(t: torch.Tensor, shape, dtype, what: str) -> int:
+    """A 2-D tensor of this shape and dtype with contiguous rows; its row stride
+    (torch leaves the stride of a single row open)."""
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
     if t.is_contiguous():
-        return
-    if not rows or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: contiguous {'rows' if t.dim() == 2 and rows else 'elements'} expected")
+        return shape[1]
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: contiguous rows expected")
+    return ld if shape[0] > 1 else max(ld, shape[1])
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor with contiguous rows (torch leaves the
-    stride of a single row open)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _matrix(t: torch.Tensor, what: str):
+    if t.dim() != 2:
+        raise ValueError(f"{what}: [rows, columns] expected, got {tuple(t.shape)}")
+    return tuple(t.shape)
 
 
-def _rows(x: torch.Tensor, what="x"):
-    if x.dim() != 2:
-        raise ValueError(f"{what}: [rows, columns] expected, got {tuple(x.shape)}")
-    _expect(x, x.shape, x.dtype, what)
-    return x.shape
-
-
-def _codes(x, q, scales):
-    M, D = x.shape
+def _codes(x, shape, q, scales):
+    """Codes and scales for rows like x's, made where not given, and the codes' row stride."""
     if q is None:
-        q = torch.empty((M, D), dtype=torch.int8, device=x.device)
+        q, ldq = x.new_empty(shape, dtype=torch.int8), shape[1]
     else:
-        _expect(q, (M, D), torch.int8, "q")
+        ldq = _rows(q, shape, torch.int8, "q")
     if scales is None:
-        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+        scales = x.new_empty(shape[0], dtype=torch.float32)
     else:
-        _expect(scales, (M,), torch.float32, "scales")
-    return q, scales
+        _expect(scales, shape[:1], torch.float32, "scales")
+    return q, ldq, scales
 
 
 def quantize_i8(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
@@ -424,12 +430,12 @@ def quantize_i8(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Te
     (q int8 [M, D], scales fp32 [M]) with x ~ q * scales[:, None]
     (fs_quantize_i8). Brings an LM head [V, D] to 8 bits (once, when it is
     loaded) and hidden states that are normed already."""
-    M, D = _rows(x)
-    dt = _dtype_code(x.dtype)
+    shape = _matrix(x, "x")
+    dt, ldx = _dtype_code(x.dtype), _rows(x, shape, x.dtype, "x")
     device = _same_device(x, q, scales)
     with _on(device, stream):
-        q, scales = _codes(x, q, scales)
-        st = _lib.fs_quantize_i8(x.data_ptr(), _ld(x), dt, M, D, q.data_ptr(), _ld(q), scales.data_ptr(),
+        q, ldq, scales = _codes(x, shape, q, scales)
+        st = _lib.fs_quantize_i8(x.data_ptr(), ldx, dt, *shape, q.data_ptr(), ldq, scales.data_ptr(),
                                  _raw_stream(device.index))
     _check(st, "fs_quantize_i8")
     return q, scales
@@ -442,39 +448,35 @@ def rms_norm_i8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual
     and one scale per row (fs_rms_norm_i8): (q, scales), and with a residual
     (q, scales, h), h = x + residual in x's dtype. h goes to sum_out if given,
     which may be x or residual itself. gain is in x's dtype or fp32."""
-    M, D = _rows(x)
-    dt = _dtype_code(x.dtype)
-    _expect(gain, (D,), gain.dtype, "gain")
+    shape = _matrix(x, "x")
+    dt, ldx = _dtype_code(x.dtype), _rows(x, shape, x.dtype, "x")
+    _expect(gain, shape[1:], gain.dtype, "gain")
     gt = _dtype_code(gain.dtype)
+    res = ldr = into = ldi = 0
     if residual is not None:
-        _expect(residual, (M, D), x.dtype, "residual")
+        res, ldr = residual.data_ptr(), _rows(residual, shape, x.dtype, "residual")
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
     device = _same_device(x, gain, residual, sum_out, q, scales)
     with _on(device, stream):
         if residual is not None:
             if sum_out is None:
-                sum_out = torch.empty((M, D), dtype=x.dtype, device=x.device)
-            else:
-                _expect(sum_out, (M, D), x.dtype, "sum_out")
-        q, scales = _codes(x, q, scales)
-        st = _lib.fs_rms_norm_i8(x.data_ptr(), _ld(x), None if residual is None else residual.data_ptr(),
-                                 0 if residual is None else _ld(residual), gain.data_ptr(), gt, dt, M, D, float(eps),
-                                 None if residual is None else sum_out.data_ptr(),
-                                 0 if residual is None else _ld(sum_out), q.data_ptr(), _ld(q), scales.data_ptr(),
-                                 _raw_stream(device.index))
+                sum_out = x.new_empty(shape)
+            into, ldi = sum_out.data_ptr(), _rows(sum_out, shape, x.dtype, "sum_out")
+        q, ldq, scales = _codes(x, shape, q, scales)
+        st = _lib.fs_rms_norm_i8(x.data_ptr(), ldx, res, ldr, gain.data_ptr(), gt, dt, *shape, eps, into, ldi,
+                                 q.data_ptr(), ldq, scales.data_ptr(), _raw_stream(device.index))
     _check(st, "fs_rms_norm_i8")
     return (q, scales) if residual is None else (q, scales, sum_out)
 
 
 def _product_inputs(q, q_scales, w, w_scales):
-    M, K = _rows(q, "q")
-    N = w.shape[0]
-    _expect(q, (M, K), torch.int8, "q")
-    _expect(w, (N, K), torch.int8, "w")
+    """(M, N, K) and the row strides of checked operands."""
+    (M, K), (N, _) = _matrix(q, "q"), _matrix(w, "w")
+    ldq, ldw = _rows(q, (M, K), torch.int8, "q"), _rows(w, (N, K), torch.int8, "w")
     _expect(q_scales, (M,), torch.float32, "q_scales")
     _expect(w_scales, (N,), torch.float32, "w_scales")
-    return M, N, K
+    return M, N, K, ldq, ldw
 
 
 def matmul_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
@@ -482,17 +484,16 @@ def matmul_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     """(q * q_scales[:, None]) @ (w * w_scales[:, None]).T of 8-bit codes q
     [M, K] and w [N, K], summed exactly in integers (fs_matmul_i8): [M, N] in
     out's dtype, or out_dtype (bf16 or fp32). K is a multiple of 16."""
-    M, N, K = _product_inputs(q, q_scales, w, w_scales)
+    M, N, K, ldq, ldw = _product_inputs(q, q_scales, w, w_scales)
     device = _same_device(q, q_scales, w, w_scales, out)
     with _on(device, stream):
         if out is None:
-            dt = _dtype_code(out_dtype)
-            out = torch.empty((M, N), dtype=out_dtype, device=q.device)
+            dt, ldo = _dtype_code(out_dtype), N
+            out = q.new_empty((M, N), dtype=out_dtype)
         else:
-            _expect(out, (M, N), out.dtype, "out")
-            dt = _dtype_code(out.dtype)
-        st = _lib.fs_matmul_i8(q.data_ptr(), _ld(q), q_scales.data_ptr(), w.data_ptr(), _ld(w), w_scales.data_ptr(),
-                               M, N, K, out.data_ptr(), _ld(out), dt, _raw_stream(device.index))
+            dt, ldo = _dtype_code(out.dtype), _rows(out, (M, N), out.dtype, "out")
+        st = _lib.fs_matmul_i8(q.data_ptr(), ldq, q_scales.data_ptr(), w.data_ptr(), ldw, w_scales.data_ptr(),
+                               M, N, K, out.data_ptr(), ldo, dt, _raw_stream(device.index))
     _check(st, "fs_matmul_i8")
     return out
 
@@ -507,7 +508,7 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     """One token per row from softmax(l / T), l = matmul_i8's fp32 logits of
     codes q [B, D] and an 8-bit LM head w [V, D] (fs_sample_i8). Noise, ties
     and NaN rule are sample_fused's."""
-    B, V, D = _product_inputs(q, q_scales, w, w_scales)
+    B, V, D, ldq, ldw = _product_inputs(q, q_scales, w, w_scales)
     device = _same_device(q, q_scales, w, w_scales, out, workspace)
     with _on(device, stream):
         if out is None:
@@ -516,7 +517,7 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
             _expect(out, (B,), torch.int32, "out")
         if workspace is None:
             workspace = torch.empty(max(sample_i8_workspace_bytes(B, D, V), 256), dtype=torch.uint8, device=q.device)
-        st = _lib.fs_sample_i8(q.data_ptr(), _ld(q), q_scales.data_ptr(), w.data_ptr(), _ld(w), w_scales.data_ptr(),
+        st = _lib.fs_sample_i8(q.data_ptr(), ldq, q_scales.data_ptr(), w.data_ptr(), ldw, w_scales.data_ptr(),
                                B, D, V, float(temperature), int(seed), int(step), workspace.data_ptr(),
                                workspace.numel() * workspace.element_size(), out.data_ptr(), _raw_stream(device.index))
     _check(st, "fs_sample_i8")
@@ -536,36 +537,33 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
     first (fs_beam_select). A beam marked in finished (bool or uint8
     [B, beams]) stands for itself once, with pad_token. out: the three output
     tensors."""
-    if scores.dim() != 2:
-        raise ValueError(f"scores [B, beams] expected, got {tuple(scores.shape)}")
-    B, beams = scores.shape
-    _expect(scores, (B, beams), torch.float32, "scores", rows=False)
-    if logits.dim() != 2 or logits.shape[0] != B * beams:
-        raise ValueError(f"logits [{B * beams}, V] expected, got {tuple(logits.shape)}")
-    _rows(logits, "logits")
-    dt = _dtype_code(logits.dtype)
-    V = logits.shape[1]
+    B, beams = _matrix(scores, "scores")
+    _expect(scores, (B, beams), torch.float32, "scores")
+    R, V = shape = _matrix(logits, "logits")
+    if R != B * beams:
+        raise ValueError(f"logits: {B * beams} rows expected, got {R}")
+    dt, ld = _dtype_code(logits.dtype), _rows(logits, shape, logits.dtype, "logits")
     n = beams if n is None else int(n)
+    done = 0
     if finished is not None:
         if finished.dtype not in (torch.bool, torch.uint8):
             raise ValueError(f"finished: bool or uint8 expected, got {finished.dtype}")
-        _expect(finished, (B, beams), finished.dtype, "finished", rows=False)
+        _expect(finished, (B, beams), finished.dtype, "finished")
+        done = finished.data_ptr()
     given = out if out is not None else ()
     device = _same_device(logits, scores, finished, workspace, *given)
     with _on(device, stream):
         if out is None:
-            out = (torch.empty((B, n), dtype=torch.float32, device=logits.device),
-                   torch.empty((B, n), dtype=torch.int32, device=logits.device),
-                   torch.empty((B, n), dtype=torch.int32, device=logits.device))
+            out = (logits.new_empty((B, n), dtype=torch.float32), logits.new_empty((B, n), dtype=torch.int32),
+                   logits.new_empty((B, n), dtype=torch.int32))
         else:
             for t, dtype, what in zip(out, (torch.float32, torch.int32, torch.int32),
                                       ("out scores", "out parents", "out tokens"), strict=True):
-                _expect(t, (B, n), dtype, what, rows=False)
+                _expect(t, (B, n), dtype, what)
         if workspace is None:
             nbytes = int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n, dt))
-            workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=logits.device)
-        st = _lib.fs_beam_select(logits.data_ptr(), _ld(logits), dt, scores.data_ptr(),
-                                 None if finished is None else finished.data_ptr(), int(pad_token), B, beams, V, n,
+            workspace = logits.new_empty(max(nbytes, 256), dtype=torch.uint8)
+        st = _lib.fs_beam_select(logits.data_ptr(), ld, dt, scores.data_ptr(), done, int(pad_token), B, beams, V, n,
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                  out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _raw_stream(device.index))
     _check(st, "fs_beam_select")
@@ -573,36 +571,45 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
 
 
 def _fold(dims):
-    """Dimensions (size, stride in bytes) from the outermost in, joined where
-    the next one continues the one before, those of size 1 left out."""
+    """Dimensions (size, strides in bytes of each tensor) from the outermost
+    in, joined where the next one continues the one before in every tensor,
+    those of size 1 left out."""
     folded = []
-    for size, stride in dims:
+    for size, strides in dims:
         if size == 1:
             continue
-        if folded and folded[-1][1] == size * stride:
-            folded[-1] = (folded[-1][0] * size, stride)
+        if folded and folded[-1][1] == tuple(size * s for s in strides):
+            folded[-1] = (folded[-1][0] * size, strides)
         else:
-            folded.append((size, stride))
+            folded.append((size, strides))
     return folded
 
 
-def _beam_layout(t: torch.Tensor, dim: int):
-    """(FsBeamLayout, byte offsets of the slabs that it does not reach) of a
-    state tensor whose rows are dimension dim."""
-    e = t.element_size()
-    dims = [(n, s * e) for n, s in zip(t.shape, t.stride())]
-    outer, inner = _fold(dims[:dim]), _fold(dims[dim + 1:] + [(e, 1)])
-    if inner and inner[-1][1] != 1:
-        raise ValueError(f"beam_reorder: strides {t.stride()} of {tuple(t.shape)} are not supported")
-    block = inner.pop()[0] if inner else 1
+def _beam_layouts(dim: int, *tensors: torch.Tensor):
+    """For each of some state tensors of one shape and dtype, whose rows are
+    dimension dim: its FsBeamLayout, alike but for the strides, and the byte
+    offsets of the slabs that a layout does not reach."""
+    return _layouts(dim, tensors[0].element_size(), tensors[0].shape, *(t.stride() for t in tensors))
+
+
+@functools.lru_cache(maxsize=64)   # shapes and strides of a decode loop come again
+def _layouts(dim, e, shape, *tensors):
+    dims = [(n, tuple(s * e for s in strides)) for n, strides in zip(shape, zip(*tensors))]
+    one, none = (1,) * len(tensors), (0,) * len(tensors)
+    outer, inner = _fold(dims[:dim]), _fold(dims[dim + 1:] + [(e, one)])
+    block = inner.pop()[0] if inner and inner[-1][1] == one else 1
     if len(inner) > 1:
-        raise ValueError(f"beam_reorder: strides {t.stride()} of {tuple(t.shape)} leave more than one run of blocks")
-    blocks = inner[0] if inner else (1, 0)
-    starts = [0]
-    for n, s in outer[:-1]:
-        starts = [o + i * s for o in starts for i in range(n)]
-    slab = outer[-1] if outer else (1, 0)
-    return FsBeamLayout(slab[0], slab[1], dims[dim][1], blocks[0], blocks[1], block), starts
+        raise ValueError("beam_reorder: strides " + ", ".join(map(str, tensors)) +
+                         f" of {tuple(shape)} leave more than one run of blocks")
+    blocks = inner[0] if inner else (1, none)
+    slab = outer.pop() if outer else (1, none)
+    layouts = []
+    for i in range(len(tensors)):
+        starts = [0]
+        for n, s in outer:
+            starts = [o + k * s[i] for o in starts for k in range(n)]
+        layouts.append((FsBeamLayout(slab[0], slab[1][i], dims[dim][1][i], blocks[0], blocks[1][i], block), starts))
+    return layouts
 
 
 def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=None):
@@ -615,10 +622,8 @@ def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=N
     is. out: None (in place), or like states. Returns what was written."""
     tensors = [states] if isinstance(states, torch.Tensor) else list(states)
     targets = tensors if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
-    if parents.dim() != 2:
-        raise ValueError(f"parents [B, beams] expected, got {tuple(parents.shape)}")
-    B, beams = parents.shape
-    _expect(parents, (B, beams), torch.int32, "parents", rows=False)
+    B, beams = _matrix(parents, "parents")
+    _expect(parents, (B, beams), torch.int32, "parents")
     if not tensors:
         raise ValueError("no states")
     if len(targets) != len(tensors):
@@ -635,22 +640,20 @@ def beam_reorder(states, parents: torch.Tensor, dim: int = 0, out=None, stream=N
     written = states if out is None else out
     if first.numel() == 0:
         return written
-    layout, starts = _beam_layout(first, dim)
-    src = [t.data_ptr() + s for t in tensors for s in starts]
-    to, dst = layout, src
-    if targets is not tensors:
-        to, to_starts = _beam_layout(targets[0], dim)
+    if targets is tensors or all(t.data_ptr() == u.data_ptr() and t.stride() == u.stride()
+                                 for t, u in zip(tensors, targets)):
+        (layout, starts), = _beam_layouts(dim, first)
+        to, dst = layout, None
+    else:
+        (layout, starts), (to, to_starts) = _beam_layouts(dim, first, targets[0])
         dst = [t.data_ptr() + s for t in targets for s in to_starts]
-        if dst == src:
-            to, dst = layout, src
-        elif (to.outer, to.blocks, to.block_bytes) != (layout.outer, layout.blocks, layout.block_bytes):
-            raise ValueError("beam_reorder: the outputs' strides split the rows differently from the states'")
+    src = [t.data_ptr() + s for t in tensors for s in starts]
     if len(src) > FS_BEAM_MAX_STATES:
         raise ValueError(f"beam_reorder: more than {FS_BEAM_MAX_STATES} separate buffers in one call")
     table = ctypes.c_void_p * len(src)
     with _on(device, stream):
-        st = _lib.fs_beam_reorder(table(*src), None if dst is src else table(*dst), len(src), ctypes.byref(layout),
-                                  None if dst is src else ctypes.byref(to), parents.data_ptr(), B, beams,
+        st = _lib.fs_beam_reorder(table(*src), None if dst is None else table(*dst), len(src), ctypes.byref(layout),
+                                  None if dst is None else ctypes.byref(to), parents.data_ptr(), B, beams,
                                   _raw_stream(device.index))
     _check(st, "fs_beam_reorder")
     return written

@@ -170,7 +170,7 @@ def test_layouts_name_every_byte_once(fs, shape, dim, index):
     import torch
     base = torch.arange(int(torch.tensor(shape).prod()), dtype=torch.int16).reshape(shape)
     view = base[index]
-    layout, starts = fs._beam_layout(view, dim)
+    (layout, starts), = fs._beam_layouts(dim, view)
     rows = view.shape[dim]
     seen = {}
     for s in starts:
@@ -189,11 +189,19 @@ def test_layouts_name_every_byte_once(fs, shape, dim, index):
     assert seen == want
 
 
+def test_layouts_of_two_tensors_split_alike(fs):
+    import torch
+    view = torch.zeros(2, 6, 3, 10, 8, dtype=torch.int16)[:, :, :, :7]
+    (a, sa), (b, sb) = fs._beam_layouts(1, view, torch.empty(2, 6, 3, 7, 8, dtype=torch.int16))
+    assert (a.outer, a.blocks, a.block_bytes) == (b.outer, b.blocks, b.block_bytes) == (2, 3, 112)
+    assert (a.block_stride, b.block_stride, a.row_stride, b.row_stride) == (160, 112, 480, 336) and sa == sb == [0]
+
+
 def test_layouts_that_are_refused(fs):
     import torch
     t = torch.zeros(6, 4, 5, 6, dtype=torch.int16)[:, :3, :4, :5]    # two runs of blocks
     with pytest.raises(ValueError, match="blocks"):
-        fs._beam_layout(t, 0)
+        fs._beam_layouts(0, t)
 
 
 def test_host_tensors_are_refused(fs):

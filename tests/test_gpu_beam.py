@@ -229,6 +229,14 @@ def test_reordering(fs, dtype, B, K):
         got = fs.beam_reorder(state[:, :, :, :length], _t(parents), dim=1, out=other[:, :, :, :length])
         assert got.data_ptr() == other.data_ptr()
         assert np.array_equal(_np(other), want_other)
+        compact = _state(rng, moved.shape, dtype)      # an output of other strides
+        want_compact = _np(compact).copy()
+        fs.beam_reorder(state[:, :, :, :length], _t(parents), dim=1, out=compact)
+        for b in range(B):
+            for i in range(K):
+                if 0 <= parents[b, i] < K:
+                    want_compact[:, b * K + i] = moved[:, b * K + i]
+        assert np.array_equal(_np(compact), want_compact)
         fs.beam_reorder(state[:, :, :, :length], _t(parents), dim=1)
         assert np.array_equal(_np(state), want)
 
