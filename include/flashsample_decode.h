@@ -86,7 +86,7 @@ fs_status_t fs_sample_i8(const int8_t* Q, int64_t ldq, const float* q_scales, co
  * scores; equal rows have equal sums whatever their place.
  *   finished: null, or uint8 [B, beams]: a beam whose entry is not zero is not
  *     continued; it stands for itself once, as (k, pad_token, score[b, k]).
- *   n: 1 .. 64; beams: 1 .. 64; 0 <= pad_token < V.
+ *   n: 1 .. 64; beams: 1 .. 64; V <= 2^31 - 2^15; 0 <= pad_token < V.
  *   out_scores fp32, out_parents (k) and out_tokens (v) int32: [B, n] each.
  * A beam with score -inf or NaN is not in use; its logits are not read. A
  * logit of -inf never follows; NaN logits are skipped, in the sum too; +inf

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxRows = 0x7FFFFFFF;
 constexpr int64_t kMaxV = 0x7FFFFFFF;          // tokens are int32
+constexpr int64_t kMaxSelectV = 0x7FFF8000;    // a chunk's end fits int32
 constexpr int64_t kMaxRowBytes = 159 * 1024;   // a row held in registers by one workgroup
 constexpr int64_t kMaxK = 131056;              // 2^31 / 2^14 - 1, a multiple of 16: no int32 sum overflows
 constexpr int64_t kMaxLd = 1 << 24;            // row offsets within a tile of 256 rows fit 32 bits
@@ -78,7 +79,7 @@ size_t sample_bytes(int64_t B, int64_t V) {
 }
 
 bool select_sizes_ok(int64_t B, int64_t beams, int64_t V, int64_t n) {
-  return B > 0 && B <= kMaxGroups && beams > 0 && beams <= FS_BEAM_MAX && V > 0 && V <= kMaxV && n > 0 &&
+  return B > 0 && B <= kMaxGroups && beams > 0 && beams <= FS_BEAM_MAX && V > 0 && V <= kMaxSelectV && n > 0 &&
          n <= FS_BEAM_MAX;
 }
 

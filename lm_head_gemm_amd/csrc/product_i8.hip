@@ -326,19 +326,23 @@ hipError_t go(const ProductI8Args& a, hipStream_t stream) {
 
 }  // namespace
 
-// The tile by the number of tiles it leaves. A launch wants most of the 256 CUs
-// busy; beyond that, larger tiles move fewer bytes per product. Measured (us,
+// The tile by the number of tiles it leaves: a launch wants most of the 256 CUs
+// busy; beyond that, larger tiles move fewer bytes per product, but write out
+// with nothing beside them on their CU, which short sums feel. Measured (us,
 // M x N x K; the tile taken first, channels x tokens):
 //   M <= 16: 64 x 16 from N = 16384 on (16 x 16384 x 4096: 12.4, small 15.8;
 //     1 x 128256 x 4096: 80), else the small kernel (1 x 5003 x 4096: 7.6, 11.5)
 //   M <= 32: 128 x 32 (32 x 128256 x 4096: 83, with 128 x 64 tiles 88)
 //   64 x 152064 x 3584: 128 x 64 100, 256 x 64 116, 64 x 64 123
 //   128 x 128256 x 4096: 256 x 128 118, 128 x 128 134
-//   1024 x 16384 x 4096: 256 x 256 75, 128 x 128 81; 1024 x 5003 x 2320:
-//     128 x 128 27, 256 x 256 47; 300 x 5003 x 512: 128 x 64 7.3, 128 x 128 9.1,
-//     32 x 64 9.7; 128 x 5003 x 4096: 32 x 64 14.8, 128 x 64 22.8, small 29.7
-//   45 x 5003 x 2320: small 8.5, 32 x 64 9.7
-// Rings of three or four stages and two workgroups per CU (one for the two
+//   1024 x 16384 x 4096: 256 x 256 75, 128 x 128 81; 1024 x 129280 x 2048: 340,
+//     410; but x 512: 128 x 128 149, 256 x 256 162; 359 x 42863 x 704: 35, 66
+//   256 x 128256 x 4096: 256 x 256 180, 128 x 128 203: with an odd number of
+//     128-token tiles below seven the larger tile's empty half costs more
+//   1024 x 5003 x 2320: 128 x 128 27, 256 x 256 47; 300 x 5003 x 512: 128 x 64
+//     7.3, 128 x 128 9.1, 32 x 64 9.7; 128 x 5003 x 4096: 32 x 64 14.8, 128 x 64
+//     22.8, small 29.7; 45 x 5003 x 2320: small 8.5, 32 x 64 9.7
+// Rings of two to four stages and two workgroups per CU (one for the two
 // largest tiles, whose LDS holds no more): deeper rings with one workgroup
 // measured 5-15% slower on the memory-bound shapes, stages of half the length
 // 5-25% slower.
@@ -349,8 +353,12 @@ hipError_t launch_product_i8(const ProductI8Args& a, hipStream_t stream) {
     return go_small<1>(a, stream);
   }
   if (a.M <= 32 && tiles(128, 32) >= 192) return go<2, 2, 4, 1, 128, 4, true>(a, stream);
-  if (a.M > 128 && tiles(256, 256) >= 192) return go<4, 8, 4, 2, 128, 2, false>(a, stream);
-  if (a.M > 64 && a.M <= 128 && tiles(256, 128) >= 192) return go<4, 4, 4, 2, 128, 3, true>(a, stream);
+  if (a.M > 64 && a.K >= 1024) {
+    const int64_t halves = ((int64_t)a.M + 127) / 128;
+    if (halves == 1 && tiles(256, 128) >= 192) return go<4, 4, 4, 2, 128, 3, true>(a, stream);
+    if (halves > 1 && (halves % 2 == 0 || halves >= 7) && tiles(256, 256) >= 192)
+      return go<4, 8, 4, 2, 128, 2, false>(a, stream);
+  }
   if (a.M > 64 && tiles(128, 128) >= 192) return go<2, 4, 4, 2, 128, 2, false>(a, stream);
   if (tiles(128, 64) >= 192)
     return a.M <= 64 ? go<2, 2, 4, 2, 128, 3, true>(a, stream) : go<2, 2, 4, 2, 128, 3, false>(a, stream);

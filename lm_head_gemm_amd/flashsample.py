@@ -544,6 +544,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
         raise ValueError(f"logits: {B * beams} rows expected, got {R}")
     dt, ld = _dtype_code(logits.dtype), _rows(logits, shape, logits.dtype, "logits")
     n = beams if n is None else int(n)
+    if not -2**31 <= pad_token < 2**31:
+        raise ValueError(f"pad_token {pad_token} is no token")
     done = 0
     if finished is not None:
         if finished.dtype not in (torch.bool, torch.uint8):

@@ -101,7 +101,7 @@ SELECT = dict(logits=FAKE, ld=1000, dtype=BF16, scores=FAKE, finished=None, pad=
     (dict(logits=None), INVALID), (dict(scores=None), INVALID), (dict(ws=None), INVALID), (dict(s=None), INVALID),
     (dict(p=None), INVALID), (dict(t=None), INVALID), (dict(B=0), INVALID), (dict(B=65537), INVALID),
     (dict(beams=0), INVALID), (dict(beams=65), INVALID), (dict(V=0), INVALID), (dict(V=2**31), INVALID),
-    (dict(n=0), INVALID), (dict(n=65), INVALID), (dict(ld=999), INVALID), (dict(pad=-1), INVALID),
+    (dict(V=2**31 - 1, ld=2**31), INVALID), (dict(n=0), INVALID), (dict(n=65), INVALID), (dict(ld=999), INVALID), (dict(pad=-1), INVALID),
     (dict(pad=1000), INVALID), (dict(dtype=3), UNSUPPORTED), (dict(logits=FAKE + 1), UNSUPPORTED),
     (dict(logits=FAKE + 2, dtype=F32), UNSUPPORTED), (dict(ws=FAKE + 8), UNSUPPORTED),
     (dict(scores=FAKE + 2), UNSUPPORTED), (dict(s=FAKE + 1), UNSUPPORTED), (dict(p=FAKE + 2), UNSUPPORTED),
@@ -231,6 +231,7 @@ def test_shapes_and_types_are_refused(fs):
             (lambda: fs.beam_select(x, s), ValueError), (lambda: fs.beam_select(x, torch.zeros(3, 1)), ValueError),
             (lambda: fs.beam_select(x, torch.zeros(2, 1).double()), ValueError),
             (lambda: fs.beam_select(x, torch.zeros(2, 1), finished=torch.zeros(2, 1)), ValueError),
+            (lambda: fs.beam_select(x, torch.zeros(2, 1), pad_token=2**32), ValueError),
             (lambda: fs.beam_reorder(x, i.long()), ValueError), (lambda: fs.beam_reorder([x, x.float()], i), ValueError),
             (lambda: fs.beam_reorder([], i), ValueError), (lambda: fs.beam_reorder(x, i, dim=1), ValueError),
             (lambda: fs.beam_reorder(x, i, out=[x, x]), ValueError)):

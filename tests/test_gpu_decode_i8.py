@@ -218,9 +218,9 @@ def test_product_k(fs, M, K):
     _check_product(fs, *_product_case(np.random.default_rng(M + K), M, 700, K, full=True))
 
 
-@pytest.mark.parametrize("K", [16, 144, 400, 768])
+@pytest.mark.parametrize("K", [16, 144, 400, 768, 1040, 1360])
 @pytest.mark.parametrize("M,N", [(3, 16400), (20, 33001), (33, 33001), (64, 74001), (100, 50001), (129, 25001),
-                                 (300, 9001), (300, 25001), (520, 24500)])
+                                 (300, 9001), (300, 25001), (500, 25001), (850, 12001)])
 def test_product_many_channels(fs, M, N, K):
     """Enough channels for each of the larger tiles, the last one ragged."""
     _check_product(fs, *_product_case(np.random.default_rng(M + N + K), M, N, K))
