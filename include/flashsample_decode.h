@@ -59,7 +59,7 @@ fs_status_t fs_rms_norm_i8(const void* X, int64_t ldx, const void* residual, int
  * one rounding to out_dtype.
  *   Q: int8 [M, K], stride ldq; W: int8 [N, K], stride ldw. Both 16-byte
  *     aligned; K, ldq, ldw multiples of 16; K <= 131056 (no sum of products
- *     of 8-bit values can overflow); ldq, ldw < 2^24.
+ *     of 8-bit values can overflow); ldq, ldw < 2^24; M, N <= 2^31 - 2^16.
  *   out: [M, N] in out_dtype (bf16 or fp32), stride ldo >= N, any alignment of
  *     the element type. */
 fs_status_t fs_matmul_i8(const int8_t* Q, int64_t ldq, const float* q_scales, const int8_t* W, int64_t ldw,
@@ -88,6 +88,8 @@ fs_status_t fs_sample_i8(const int8_t* Q, int64_t ldq, const float* q_scales, co
  *     continued; it stands for itself once, as (k, pad_token, score[b, k]).
  *   n: 1 .. 64; beams: 1 .. 64; V <= 2^31 - 2^15; 0 <= pad_token < V.
  *   out_scores fp32, out_parents (k) and out_tokens (v) int32: [B, n] each.
+ *     out_scores may be `scores` itself where n == beams; no other overlap of
+ *     buffers is allowed.
  * A beam with score -inf or NaN is not in use; its logits are not read. A
  * logit of -inf never follows; NaN logits are skipped, in the sum too; +inf
  * leaves its beam without continuation. Where fewer than n continuations

@@ -10,7 +10,7 @@ namespace fs {
 namespace {
 
 constexpr int64_t kMaxRows = 0x7FFFFFFF;
-constexpr int64_t kMaxV = 0x7FFFFFFF;          // tokens are int32
+constexpr int64_t kMaxTiled = 0x7FFF0000;      // rows and channels of a product: a tile's or part's end fits int32
 constexpr int64_t kMaxSelectV = 0x7FFF8000;    // a chunk's end fits int32
 constexpr int64_t kMaxRowBytes = 159 * 1024;   // a row held in registers by one workgroup
 constexpr int64_t kMaxK = 131056;              // 2^31 / 2^14 - 1, a multiple of 16: no int32 sum overflows
@@ -42,7 +42,7 @@ fs_status_t check_rows(const void* X, int64_t ldx, int dtype, int64_t M, int64_t
 fs_status_t check_product(const int8_t* Q, int64_t ldq, const float* q_scales, const int8_t* W, int64_t ldw,
                           const float* w_scales, int64_t M, int64_t N, int64_t K) {
   if (!Q || !q_scales || !W || !w_scales) return FS_ERR_INVALID_ARGUMENT;
-  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || N > kMaxV || ldq < K || ldw < K) return FS_ERR_INVALID_ARGUMENT;
+  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxTiled || N > kMaxTiled || ldq < K || ldw < K) return FS_ERR_INVALID_ARGUMENT;
   if (K > kMaxK || K % 16 || ldq % 16 || ldw % 16 || ldq >= kMaxLd || ldw >= kMaxLd) return FS_ERR_UNSUPPORTED;
   if (!aligned(Q, 16) || !aligned(W, 16) || !aligned(q_scales, 4) || !aligned(w_scales, 4)) return FS_ERR_UNSUPPORTED;
   return FS_OK;
@@ -70,7 +70,7 @@ ProductI8Args product_args(const int8_t* Q, int64_t ldq, const float* q_scales, 
 // Workspace of fs_sample_i8: fp32 logits [B, V rounded up to 8], then the
 // sampler's partial keys.
 bool sample_sizes_ok(int64_t B, int64_t D, int64_t V) {
-  return B > 0 && D > 0 && V > 0 && B <= kMaxGroups && D <= kMaxK && V <= kMaxV;
+  return B > 0 && D > 0 && V > 0 && B <= kMaxGroups && D <= kMaxK && V <= kMaxTiled;
 }
 int64_t sample_ld(int64_t V) { return (V + 7) / 8 * 8; }
 size_t sample_logits_bytes(int64_t B, int64_t V) { return align_up((size_t)B * sample_ld(V) * sizeof(float)); }

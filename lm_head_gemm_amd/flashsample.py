@@ -536,7 +536,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
     [B, beams]: (scores fp32, parents int32, tokens int32), each [B, n], best
     first (fs_beam_select). A beam marked in finished (bool or uint8
     [B, beams]) stands for itself once, with pad_token. out: the three output
-    tensors."""
+    tensors; the scores may go to `scores` itself where n is beams."""
     B, beams = _matrix(scores, "scores")
     _expect(scores, (B, beams), torch.float32, "scores")
     R, V = shape = _matrix(logits, "logits")

@@ -59,7 +59,8 @@ PRODUCT = dict(Q=FAKE, ldq=64, qs=FAKE, W=FAKE, ldw=64, ws=FAKE, M=4, N=100, K=6
 @pytest.mark.parametrize("kw,status", [
     (dict(Q=None), INVALID), (dict(qs=None), INVALID), (dict(W=None), INVALID), (dict(ws=None), INVALID),
     (dict(out=None), INVALID), (dict(M=0), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID),
-    (dict(N=2**31), INVALID), (dict(M=2**31), INVALID), (dict(ldq=48), INVALID), (dict(ldw=48), INVALID),
+    (dict(N=2**31), INVALID), (dict(M=2**31), INVALID), (dict(N=2**31 - 1, ldo=2**31), INVALID),
+    (dict(M=2**31 - 1), INVALID), (dict(ldq=48), INVALID), (dict(ldw=48), INVALID),
     (dict(ldo=99), INVALID), (dict(K=56), UNSUPPORTED), (dict(ldq=72), UNSUPPORTED), (dict(ldw=72), UNSUPPORTED),
     (dict(K=131072, ldq=131072, ldw=131072), UNSUPPORTED), (dict(Q=FAKE + 8), UNSUPPORTED),
     (dict(ldq=2**24), UNSUPPORTED), (dict(ldw=2**24), UNSUPPORTED),
@@ -89,7 +90,7 @@ def test_sample_refusals(fs, kw, status):
 def test_sample_workspace(fs):
     need = fs.sample_i8_workspace_bytes(4, 64, 100)
     assert need >= 4 * 104 * 4 + 4 * 8 and need % 256 == 0
-    for bad in ((0, 64, 100), (4, 0, 100), (4, 64, 0), (65537, 64, 100), (4, 131072, 100), (4, 64, 2**31)):
+    for bad in ((0, 64, 100), (4, 0, 100), (4, 64, 0), (65537, 64, 100), (4, 131072, 100), (4, 64, 2**31), (4, 64, 2**31 - 1)):
         assert fs.sample_i8_workspace_bytes(*bad) == 0
 
 

@@ -177,6 +177,38 @@ def test_strided_logits_and_given_outputs(fs):
         fs.beam_select(_t(logits), _t(scores), n, pad_token=V)
 
 
+def test_scores_in_place_in_a_replayed_graph(fs):
+    """Scores written over the ones read, as a loop captured once keeps them;
+    two graphs with a workspace of their own, replayed in turn."""
+    import torch
+    rng = np.random.default_rng(12)
+    B, K, V = 3, 8, 9001
+    logits = [_t((rng.standard_normal((B * K, V)) * 2).astype(np.float32)) for _ in range(2)]
+    start = _t((-rng.random((B, K))).astype(np.float32))
+    scores = [start.clone() for _ in range(2)]
+    outs = [[s, torch.zeros((B, K), dtype=torch.int32, device="cuda"),
+             torch.zeros((B, K), dtype=torch.int32, device="cuda")] for s in scores]
+    for l, o in zip(logits, outs):
+        fs.beam_select(l, o[0], out=o)            # eager, in place
+    want = [fs.beam_select(l, start) for l in logits]
+    assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, l, o in zip(graphs, logits, outs):
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            fs.beam_select(l, o[0], out=o)
+    for s in scores:
+        s.copy_(start)
+    state = [start, start]
+    for step in range(4):
+        for i, g in enumerate(graphs):
+            g.replay()
+            want = fs.beam_select(logits[i], state[i])
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want))
+            state[i] = want[0]
+
+
 def test_rows_past_32_bit_offsets(fs):
     import torch
     V, K = 2**20 + 3, 2
