@@ -415,7 +415,7 @@ def _matrix(t: torch.Tensor, what: str):
 def _codes(x, shape, q, scales):
     """Codes and scales for rows like x's, made where not given, and the codes' row stride."""
     if q is None:
-        q, ldq = x.new_empty(shape, dtype=torch.int8), shape[1]
+        q, ldq = x.new_empty(*shape, dtype=torch.int8), shape[1]
     else:
         ldq = _rows(q, shape, torch.int8, "q")
     if scales is None:
@@ -461,7 +461,7 @@ def rms_norm_i8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6, residual
     with _on(device, stream):
         if residual is not None:
             if sum_out is None:
-                sum_out = x.new_empty(shape)
+                sum_out = x.new_empty(*shape)
             into, ldi = sum_out.data_ptr(), _rows(sum_out, shape, x.dtype, "sum_out")
         q, ldq, scales = _codes(x, shape, q, scales)
         st = _lib.fs_rms_norm_i8(x.data_ptr(), ldx, res, ldr, gain.data_ptr(), gt, dt, *shape, eps, into, ldi,
@@ -489,7 +489,7 @@ def matmul_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     with _on(device, stream):
         if out is None:
             dt, ldo = _dtype_code(out_dtype), N
-            out = q.new_empty((M, N), dtype=out_dtype)
+            out = q.new_empty(M, N, dtype=out_dtype)
         else:
             dt, ldo = _dtype_code(out.dtype), _rows(out, (M, N), out.dtype, "out")
         st = _lib.fs_matmul_i8(q.data_ptr(), ldq, q_scales.data_ptr(), w.data_ptr(), ldw, w_scales.data_ptr(),
@@ -524,6 +524,11 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
     return out
 
 
+@functools.lru_cache(maxsize=64)   # by sizes only
+def _select_bytes(B, beams, V, n, dt) -> int:
+    return max(int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n, dt)), 256)
+
+
 def beam_select_workspace_bytes(B, beams, V, n, dtype=torch.bfloat16) -> int:
     return int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n, _dtype_code(dtype)))
 
@@ -556,15 +561,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
     device = _same_device(logits, scores, finished, workspace, *given)
     with _on(device, stream):
         if out is None:
-            out = (logits.new_empty((B, n), dtype=torch.float32), logits.new_empty((B, n), dtype=torch.int32),
-                   logits.new_empty((B, n), dtype=torch.int32))
+            out = (logits.new_empty(B, n, dtype=torch.float32), logits.new_empty(B, n, dtype=torch.int32),
+                   logits.new_empty(B, n, dtype=torch.int32))
         else:
             for t, dtype, what in zip(out, (torch.float32, torch.int32, torch.int32),
                                       ("out scores", "out parents", "out tokens"), strict=True):
                 _expect(t, (B, n), dtype, what)
         if workspace is None:
-            nbytes = int(_lib.fs_beam_select_workspace_bytes(B, beams, V, n, dt))
-            workspace = logits.new_empty(max(nbytes, 256), dtype=torch.uint8)
+            workspace = logits.new_empty(_select_bytes(B, beams, V, n, dt), dtype=torch.uint8)
         st = _lib.fs_beam_select(logits.data_ptr(), ld, dt, scores.data_ptr(), done, int(pad_token), B, beams, V, n,
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                  out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _raw_stream(device.index))
