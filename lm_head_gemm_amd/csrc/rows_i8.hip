@@ -8,15 +8,22 @@
 // The norm's factor rstd is common to the row and cancels out of the codes, so
 // no code depends on a sum. What is left is to round an exact quotient: the
 // product u of two 16-bit values is exact in fp32, the product with an fp32
-// gain in fp64. Each code is first taken from the fp32 product with 127 / a
-// (error below 3e-5 steps); one within 1e-4 of the middle between two codes is
-// taken again from the fp64 quotient. Rows whose largest value fp32 products
-// may have rounded or lost (outside 2^-100 .. 2^126, zero rows, NaN and
-// infinity) are done in fp64 throughout.
+// gain in fp64. Each code is first taken from fp32 products with 127 / a (off
+// by at most four roundings, 127 x 2^-22 = 3.1e-5 steps); one within 1e-4 of the
+// middle between two codes is taken again from the fp64 quotient, whose a is
+// exact: with an fp32 gain, the largest fp64 product among those whose fp32
+// product comes within 2^-22 of the largest. Rows whose largest value fp32
+// products may have lost (outside 2^-100 .. 2^126, zero rows, NaN and infinity)
+// are done in fp64 throughout.
 //
 // Bound: memory (x, residual and gain read, h, codes and scales written once).
 // The row stays in registers between the reduction and the codes: G threads
-// hold V 16-byte pieces each, so a row is read once whatever its length.
+// hold V 16-byte pieces each, so a row is read once whatever its length. Gains
+// are fetched beside the row: read between the stores of h and of codes, which
+// no load may pass, they cost 10-40% of the time.
+// Measured: norm with residual, bf16, 4099 x 8192 48.3 us (4.9 TB/s read and
+// written, a large copy's rate), with an fp32 gain 54 us; 64 x 7168 4.8 us, 1 x
+// 4096 3.8 us; codes of 128256 x 4096 bf16 256 us (6.2 TB/s).
 #include "fs_decode.h"
 
 namespace fs {
@@ -98,6 +105,27 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
     h[v] = make_uint4(0u, 0u, 0u, 0u);
     if (p < np) h[v] = load_stream16(x + p);
   }
+  // gain of piece p, value e
+  auto gain_of = [&](int p, int e) -> float {
+    if constexpr (GAIN == 1) return piece_value<true>(static_cast<const uint4*>(a.gain)[p], e);
+    if constexpr (GAIN == 2) return static_cast<const float*>(a.gain)[(int64_t)p * E + e];
+    return 1.0f;
+  };
+  // The gains, fetched beside the row, then the fp32 products; where a thread's
+  // registers do not hold them too, gains are read at each use.
+  constexpr bool kKeep = GAIN != 0 && V <= 4;
+  float u[kKeep ? V : 1][E];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = tid + v * G;
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[v][e] = 0.0f;
+      if (p < np)
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[v][e] = gain_of(p, e);
+    }
+  }
   if constexpr (RES) {
     const uint4* r = reinterpret_cast<const uint4*>(static_cast<const char*>(a.residual) + row * a.ldr * (16 / E));
     uint4* s = reinterpret_cast<uint4*>(static_cast<char*>(a.sum) + row * a.lds * (16 / E));
@@ -126,17 +154,22 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
     }
   }
 
-  // gain of piece p, value e; read again for the codes (it stays in cache)
-  auto gain_of = [&](int p, int e) -> float {
-    if constexpr (GAIN == 1) return piece_value<true>(static_cast<const uint4*>(a.gain)[p], e);
-    if constexpr (GAIN == 2) return static_cast<const float*>(a.gain)[(int64_t)p * E + e];
-    return 1.0f;
-  };
-  auto value = [&](auto zero, int v, int e, int p) {
-    using U = decltype(zero);
-    const U f = (U)piece_value<BF16>(h[v], e);
+  // u exactly; the few values that need it read their gain again
+  auto exact = [&](int v, int e, int p) -> double {
+    const double f = (double)piece_value<BF16>(h[v], e);
     if constexpr (GAIN == 0) return f;
-    else return f * (U)gain_of(p, e);
+    else return f * (double)gain_of(p, e);
+  };
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[v][e] *= piece_value<BF16>(h[v], e);
+  }
+  auto value = [&](int v, int e, int p) -> float {
+    if constexpr (kKeep) return u[v][e];
+    else if constexpr (GAIN == 0) return piece_value<BF16>(h[v], e);
+    else return piece_value<BF16>(h[v], e) * gain_of(p, e);
   };
 
   double rstd = 1.0;
@@ -164,22 +197,38 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
     else *reinterpret_cast<uint32_t*>(codes + (int64_t)p * E) = w[0];
   };
 
-  if constexpr (GAIN != 2) {
-    uint32_t top = 0u;
+  // the row's largest |u| as an fp64 number, of all values or of those whose fp32 product reaches `least`
+  auto largest = [&](auto all_c, float least) -> uint64_t {
+    uint64_t top = 0u;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int p = tid + v * G;
       if (p < np)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t m = magnitude(value(0.0f, v, e, p));
-          top = m > top ? m : top;
-        }
+        for (int e = 0; e < E; ++e)
+          if (decltype(all_c)::value || fabsf(value(v, e, p)) >= least) {
+            const uint64_t m = magnitude(exact(v, e, p));
+            top = m > top ? m : top;
+          }
     }
-    top = row_max<G>(top, reinterpret_cast<uint32_t*>(red_max), tid);
-    if (top >= 0x0D800000u && top < 0x7E800000u) {   // 2^-100 <= a < 2^126 (uniform over the row)
-      const float amax = __uint_as_float(top);
-      const float inv = 127.0f / amax;
+    return row_max<G>(top, red_max, tid);
+  };
+  if constexpr (GAIN != 2 || kKeep) {
+    uint32_t top32 = 0u;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int p = tid + v * G;
+      if (GAIN == 0 || kKeep || p < np)   // else: pieces past the row are zero
+#pragma unroll
+        for (int e = 0; e < E; ++e) top32 = max(top32, magnitude(value(v, e, p)));
+    }
+    top32 = row_max<G>(top32, reinterpret_cast<uint32_t*>(red_max), tid);
+    if (top32 >= 0x0D800000u && top32 < 0x7E800000u) {   // 2^-100 <= a < 2^126 (uniform over the row)
+      const float a32 = __uint_as_float(top32);
+      double amax = (double)a32;
+      // rounded products: the exact largest is among those within 2^-22
+      if constexpr (GAIN == 2) amax = __longlong_as_double((long long)largest(std::false_type{}, a32 * (1.0f - 0x1p-22f)));
+      const float inv = 127.0f / a32;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int p = tid + v * G;
@@ -187,33 +236,21 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
           int c[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float u = value(0.0f, v, e, p);
-            const float t = u * inv;
+            const float t = value(v, e, p) * inv;
             float k = rintf(t);
-            if (fabsf(t - k) > 0.4999f) k = (float)rint(127.0 * (double)u / (double)amax);
+            if (fabsf(t - k) > 0.4999f) k = (float)rint(127.0 * (GAIN == 2 ? exact(v, e, p) : (double)value(v, e, p)) / amax);
             c[e] = (int)k;
           }
           store(p, c);
         }
       }
-      if (tid == 0) a.scales[row] = (float)((double)amax * rstd / 127.0);
+      if (tid == 0) a.scales[row] = (float)(amax * rstd / 127.0);
       return;
     }
   }
 
-  // fp64 throughout: fp32 gains, and rows outside fp32's range above
-  uint64_t top = 0u;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int p = tid + v * G;
-    if (p < np)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint64_t m = magnitude(value(0.0, v, e, p));
-        top = m > top ? m : top;
-      }
-  }
-  top = row_max<G>(top, red_max, tid);
+  // rows outside fp32's range above, and long ones with fp32 gains: fp64 throughout
+  const uint64_t top = largest(std::true_type{}, 0.0f);
   const double amax = __longlong_as_double((long long)top);
   const bool bad = top >= 0x7FF0000000000000ull;   // a NaN or an infinity
   const bool none = bad || top == 0u;
@@ -225,10 +262,10 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
       int c[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const double u = value(0.0, v, e, p);
-        const double t = u * inv;
+        const double x64 = exact(v, e, p);
+        const double t = x64 * inv;
         double k = rint(t);
-        if (fabs(t - k) > 0.4999) k = rint(127.0 * u / amax);
+        if (fabs(t - k) > 0.4999) k = rint(127.0 * x64 / amax);
         c[e] = none ? 0 : (int)k;
       }
       store(p, c);
@@ -244,14 +281,22 @@ hipError_t go(const RowsI8Args& a, hipStream_t stream) {
   return launch(rows_i8_kernel<BF16, GAIN, RES, G, V>, dim3((unsigned)blocks), dim3(G < 256 ? 256 : G), 0, stream, a);
 }
 
-// Threads and pieces per row by its length alone: a wave for short rows (no
-// barrier), 256 threads up to 1024 pieces (16 KiB), 1024 threads above.
+// Threads and pieces per row: a wave for short rows (no barrier), 256 threads up
+// to 1024 pieces (16 KiB), 1024 threads above. With no more rows than CUs a
+// row has its CU to itself: a thread per piece. Measured (us, bf16, residual):
+// 64 x 7168 1024 threads 4.8, 256 6.5; 256 x 8192 5.7, 7.4; 1 x 4096 512 threads
+// 3.8, 256 4.4 (300 rows: 5.6 either way). 4096 x 5120 three pieces per thread
+// 34.0, four 40.9; 4099 x 8192 256 threads of four 48.2, 512 of two 49.4 (fp32
+// gain 54, 61).
 template <bool BF16, int GAIN, bool RES>
 hipError_t by_length(const RowsI8Args& a, hipStream_t stream) {
   const int64_t np = (int64_t)a.D / (BF16 ? 8 : 4);
   if (np <= 64) return go<BF16, GAIN, RES, 64, 1>(a, stream);
   if (np <= 256) return go<BF16, GAIN, RES, 256, 1>(a, stream);
+  if (a.M <= 256 && np > 256 && np <= 512) return go<BF16, GAIN, RES, 512, 1>(a, stream);
+  if (a.M <= 256 && np > 512 && np <= 1024) return go<BF16, GAIN, RES, 1024, 1>(a, stream);
   if (np <= 512) return go<BF16, GAIN, RES, 256, 2>(a, stream);
+  if (np <= 768) return go<BF16, GAIN, RES, 256, 3>(a, stream);
   if (np <= 1024) return go<BF16, GAIN, RES, 256, 4>(a, stream);
   if (np <= 2048) return go<BF16, GAIN, RES, 1024, 2>(a, stream);
   if (np <= 4096) return go<BF16, GAIN, RES, 1024, 4>(a, stream);

@@ -99,6 +99,54 @@ def test_norm_many_rows(fs, M):
         assert np.array_equal(h.float().cpu().numpy(), want[2])
 
 
+@pytest.mark.parametrize("bf16,D", [(True, d) for d in (2048, 2056, 4096, 4104, 6144, 6152, 8192, 8200)] +
+                         [(False, d) for d in (1028, 2048, 2052, 3076, 4096)])
+def test_norm_more_rows_than_cus(fs, bf16, D):
+    """The layouts for many rows (those for few rows are the ones above)."""
+    import torch
+    M = 257
+    rng = np.random.default_rng(D + 2)
+    t = torch.bfloat16 if bf16 else torch.float32
+    x, r = _vals(rng, (M, D), bf16), _vals(rng, (M, D), bf16, 2.0)
+    g = _vals(rng, (D,), True, 0.2) + np.float32(1)
+    for gt in (torch.bfloat16, torch.float32) if bf16 else (torch.float32,):
+        gain = decode.bf16_round(g) if gt is torch.bfloat16 else g * np.float32(1.0000123)
+        for res in (None, r):
+            want = decode.rms_norm(x, gain, 1e-5, res, bf16)
+            got = fs.rms_norm_i8(_t(x, t), _t(gain, gt), 1e-5, residual=None if res is None else _t(res, t))
+            _check_codes(got[0], got[1], want[0], want[1])
+    q, s = fs.quantize_i8(_t(x, t))
+    _check_codes(q, s, *decode.quantize(x))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_rounded_products_with_fp32_gains(fs, bf16):
+    """Products that fp32 rounds: the largest one among others that fp32 cannot
+    tell from it, and quotients beside the middle between two codes of it."""
+    import torch
+    rng = np.random.default_rng(77)
+    D, M = 1024, 40
+    t = torch.bfloat16 if bf16 else torch.float32
+    for i in range(M):
+        x = np.ones(D, dtype=np.float32)
+        g = (rng.random(D) * 0.5).astype(np.float32)
+        big = _vals(rng, (1,), bf16, 0.2)[0] % np.float32(0.5) + np.float32(1.25)
+        big = decode.bf16_round(np.array([big]))[0] if bf16 else big
+        base = np.float32(1.5 + 0.25 * rng.random())
+        x[:4] = big
+        g[:4] = base
+        g[1], g[2] = np.nextafter(base, np.float32(0)), np.nextafter(base, np.float32(9))
+        x[3], g[3] = -base if not bf16 else -big, big if not bf16 else base
+        a = np.abs(x.astype(np.float64) * g).max()
+        k = rng.integers(-126, 126, 600)
+        g[100:700] = ((k + 0.5) * a / 127.0).astype(np.float32)
+        g[100:300] = np.nextafter(g[100:300], np.float32(9))
+        g[300:500] = np.nextafter(g[300:500], np.float32(-9))
+        want = decode.rms_norm(x[None], g, 1e-5)
+        q, s = fs.rms_norm_i8(_t(x[None], t), _t(g), 1e-5)
+        _check_codes(q, s, want[0], want[1])
+
+
 def test_codes_in_the_middle(fs):
     """Quotients at, and one bit beside, the middle between two codes."""
     import torch
