@@ -10,12 +10,18 @@
 //  * merge: a workgroup per group of beams joins the chunks' sums to the rows'
 //    logarithms in fp64, scores the chunks' entries, and picks the n best.
 //
-// Both pick n of many the same way: split the values into 64 sets, take each
-// set's largest, and let t be (a little below) the n-th largest of those. At
-// least n values reach t, and usually few more do: these go to LDS, where each
-// counts the ones ahead of it. If too many reach t (long runs of equal values),
-// the scan finds the n-th value bit by bit and the merge takes the best one n
-// times.
+// Both pick n of many the same way: split the values into sets, take each set's
+// largest, and let t be (a little below) the n-th largest of those. At least n
+// values reach t, and usually few more do (of s sets, about -s ln(1 - n / s)):
+// these go to LDS, where each counts the ones ahead of it. 64 sets up to n = 32,
+// 256 above (64 of 64 would let in 300 and more: measured, n = 64, 512 rows of
+// 152064, scan 343 us, with 256 sets 42). If too many reach t (long runs of equal values), the scan finds the
+// n-th value bit by bit and the merge takes the best one n times.
+//
+// Bound: the scan by its vector instructions (busy 80% of the time on long
+// rows: an exponential, which takes four issues, and seven others per entry),
+// the merge by latency. Measured, 512 rows of 152064 bf16, groups of 8: scan 34
+// us (4.6 TB/s), merge 6; 4 rows of 128256 fp32: 5 and 6 us.
 #include "fs_decode.h"
 
 namespace fs {
@@ -29,7 +35,8 @@ constexpr int kListed = 512;              // scan: entries that may reach the bo
 constexpr int kPieces = 256;              // scan: pieces that hold such entries
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeListed = 1024;
-constexpr int kSets = 64;
+constexpr int kFewSets = 64, kSets = 256;
+constexpr int kFewN = 32;                 // largest n for the fewer sets
 constexpr int kFirst = 2;                 // merge: entries per thread fetched ahead
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -103,12 +110,16 @@ __device__ __forceinline__ float lane63(float x) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
 }
 
-// The n-th largest of the lanes' values of `bits` bits (n <= 64), in every lane.
-__device__ __forceinline__ uint32_t nth_of_lanes(uint32_t x, int bits, int n) {
+// The n-th largest of the lanes' values of `bits` bits, Q per lane (n <= 64 Q), in every lane.
+template <int Q>
+__device__ __forceinline__ uint32_t nth_of_lanes(const uint32_t (&x)[Q], int bits, int n) {
   uint32_t t = 0u;
   for (int b = bits - 1; b >= 0; --b) {
     const uint32_t probe = t | (1u << b);
-    if (__popcll(__ballot(x >= probe)) >= n) t = probe;
+    int k = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) k += __popcll(__ballot(x[q] >= probe));
+    if (k >= n) t = probe;
   }
   return t;
 }
@@ -146,6 +157,7 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a) {
   const int begin = chunk * (IT * kStep);
   const int whole = a.V & ~(kPiece - 1);   // entries in whole pieces; up to seven are left in the last chunk
   const int mine = tid * kPiece;
+  const int steps = min(IT, (a.V - begin + kStep - 1) / kStep);   // fewer in a row's last chunk
   const void* base = static_cast<const char*>(a.logits) + (int64_t)row * a.ld * (BF16 ? 2 : 4);
 
   Piece<BF16> x[IT];
@@ -163,6 +175,8 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a) {
   float top[IT], best = fmaxf(rest, -__builtin_inff());
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
+    top[it] = -__builtin_inff();
+    if (it >= steps) continue;
     top[it] = x[it].value(0);
 #pragma unroll
     for (int i = 1; i < kPiece; ++i) top[it] = fmaxf(top[it], x[it].value(i));
@@ -179,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a) {
   };
   hold();
 
-  // the sets: the threads of one lane number
+  // the sets: the threads of one lane number, or each thread by itself
   if (tid == 0) listed = n_pieces = 0;
   red_f[wave * 64 + lane] = best;
   __syncthreads();
@@ -187,7 +201,18 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a) {
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) best = fmaxf(best, red_f[w * 64 + lane]);
   const float m = lane63(over_lanes(best, -__builtin_inff(), [](float p, float q) { return fmaxf(p, q); }));
-  const float bound = number_at(nth_of_lanes((uint32_t)(pack_key(best, 0u) >> 48), 16, a.n) << 16);
+  auto place16 = [](float x) { return (uint32_t)(pack_key(x, 0u) >> 48); };
+  uint32_t nth;
+  if (a.n <= kFewN) {
+    const uint32_t sets[1] = {place16(best)};
+    nth = nth_of_lanes(sets, 16, a.n);
+  } else {
+    uint32_t sets[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sets[w] = place16(fmaxf(red_f[w * 64 + lane], -__builtin_inff()));
+    nth = nth_of_lanes(sets, 16, a.n);
+  }
+  const float bound = number_at(nth << 16);
 
   const int64_t at = (int64_t)row * a.n_chunks + chunk;
   uint64_t* out = a.cand + at * a.n;
@@ -210,9 +235,11 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a) {
     residue = fmaf(m, kLog2e, -c);
     s = __builtin_amdgcn_exp2f(fmaf(rest, kLog2e, -c));
 #pragma unroll
-    for (int it = 0; it < IT; ++it)
+    for (int it = 0; it < IT; ++it) {
+      if (it >= steps) break;
 #pragma unroll
       for (int i = 0; i < kPiece; ++i) s += __builtin_amdgcn_exp2f(fmaf(x[it].value(i), kLog2e, -c));
+    }
   }
   if (s != s || !(fabsf(m) <= kLargest)) {   // NaN among this thread's entries: without them
     residue = 0.0f;
@@ -300,12 +327,12 @@ __global__ __launch_bounds__(kThreads) void beam_scan_kernel(BeamSelectArgs a) {
     list_entries(t, before + 1);   // exactly n entries, in at most n + 1 pieces
   }
   const int c = listed;
-  // a wave takes every fourth entry and counts the ones ahead of it, 64 at a time
-  for (int j = wave; j < c; j += kWaves) {
+  for (int j = tid; j < c; j += kThreads) {   // a thread counts the ones ahead of its entry
     const uint64_t key = list[j];
     int rank = 0;
-    for (int k = lane; k - lane < c; k += 64) rank += __popcll(__ballot(k < c && list[k] > key));
-    if (rank < a.n && lane == 0) out[rank] = key;
+#pragma unroll 8
+    for (int k = 0; k < c; ++k) rank += list[k] > key;
+    if (rank < a.n) out[rank] = key;
   }
   if (tid >= c && tid < a.n) out[tid] = 0ull;
 }
@@ -415,18 +442,27 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   // The bound, from the first `ranks` entries of every chunk (about eight per
   // set at least): sets by a mixing hash, so that neither the rank nor the
   // beam of an entry decides its set.
-  const int lists = K * nc;
-  const int ranks = min(n, (8 * kSets + lists - 1) / lists);
+  const int lists = K * nc, n_sets = n <= kFewN ? kFewSets : kSets;
+  const int ranks = min(n, (8 * n_sets + lists - 1) / lists);
   each_entry([&](int j, const Scored& e) {
     if (j >= scanned || j % n < ranks) {
       uint32_t h = (uint32_t)j * 2654435769u;
       h = (h ^ (h >> 15)) * 2246822519u;
-      atomicMax(&set_best[(h ^ (h >> 13)) % kSets], (uint32_t)(e.order >> 32));
+      atomicMax(&set_best[(h ^ (h >> 13)) & (n_sets - 1)], (uint32_t)(e.order >> 32));
     }
   });
   __syncthreads();
   if (wave == 0) {   // 24 bits: sign, exponent and twelve bits of the scores
-    const uint32_t t = nth_of_lanes(set_best[lane] >> 8, 24, n);
+    uint32_t t;
+    if (n <= kFewN) {
+      const uint32_t sets[1] = {set_best[lane] >> 8};
+      t = nth_of_lanes(sets, 24, n);
+    } else {
+      uint32_t sets[kSets / 64];
+#pragma unroll
+      for (int q = 0; q < kSets / 64; ++q) sets[q] = set_best[q * 64 + lane] >> 8;
+      t = nth_of_lanes(sets, 24, n);
+    }
     if (lane == 0) set_best[0] = t << 8;
   }
   __syncthreads();
@@ -477,12 +513,12 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   float* out_scores = a.out_scores + (int64_t)b * n;
   int32_t* out_parents = a.out_parents + (int64_t)b * n;
   int32_t* out_tokens = a.out_tokens + (int64_t)b * n;
-  for (int j = wave; j < c; j += kMW) {   // a wave counts the ones ahead of an entry, 64 at a time
+  for (int j = tid; j < c; j += kMergeThreads) {   // a thread counts the ones ahead of its entry
     const Scored e{list_order[j], list_place[j]};
     int rank = 0;
-    for (int k = lane; k - lane < c; k += 64)
-      rank += __popcll(__ballot(k < c && ahead(Scored{list_order[k], list_place[k]}, e)));
-    if (rank < n && lane == 0) {
+#pragma unroll 8
+    for (int k = 0; k < c; ++k) rank += ahead(Scored{list_order[k], list_place[k]}, e);
+    if (rank < n) {
       const int beam = (int)(e.place / a.V);
       out_scores[rank] = (float)score_at(e.order);
       out_parents[rank] = beam;
