@@ -14,9 +14,10 @@
 // largest, and let t be (a little below) the n-th largest of those. At least n
 // values reach t, and usually few more do (of s sets, about -s ln(1 - n / s)):
 // these go to LDS, where each counts the ones ahead of it. 64 sets up to n = 32,
-// 256 above (64 of 64 would let in 300 and more: measured, n = 64, 512 rows of
-// 152064, scan 343 us, with 256 sets 42). If too many reach t (long runs of equal values), the scan finds the
-// n-th value bit by bit and the merge takes the best one n times.
+// 256 above: the least of 64 maxima lets in 300 and more (measured, n = 64, 512
+// rows of 152064 bf16: scan 343 us, with 256 sets 43). If too many reach t (long
+// runs of equal values), the scan finds the n-th value bit by bit and the merge
+// takes the best one n times.
 //
 // Bound: the scan by its vector instructions (busy 80% of the time on long
 // rows: an exponential, which takes four issues, and seven others per entry),
