@@ -88,8 +88,8 @@ fs_status_t fs_sample_i8(const int8_t* Q, int64_t ldq, const float* q_scales, co
  *     continued; it stands for itself once, as (k, pad_token, score[b, k]).
  *   n: 1 .. 64; beams: 1 .. 64; V <= 2^31 - 2^15; 0 <= pad_token < V.
  *   out_scores fp32, out_parents (k) and out_tokens (v) int32: [B, n] each.
- *     out_scores may be `scores` itself where n == beams; no other overlap of
- *     buffers is allowed.
+ *     out_scores may be `scores` itself where n == beams (refused if they
+ *     overlap otherwise); no other overlap of buffers is allowed.
  * A beam with score -inf or NaN is not in use; its logits are not read. A
  * logit of -inf never follows; NaN logits are skipped, in the sum too; +inf
  * leaves its beam without continuation. Where fewer than n continuations

@@ -262,6 +262,9 @@ fs_status_t fs_beam_select(const void* logits, int64_t ld_logits, fs_dtype_t log
     return FS_ERR_UNSUPPORTED;
   const SelectSpace s = select_space(B, beams, V, n, logits_dtype == FS_DTYPE_BF16);
   if (workspace_bytes < s.bytes) return FS_ERR_WORKSPACE_TOO_SMALL;
+  // a group's scores are read before its outputs are written; another group's may be read later
+  const bool in_place = scores == out_scores && n == beams;
+  if (!in_place && scores < out_scores + B * n && out_scores < scores + B * beams) return FS_ERR_INVALID_ARGUMENT;
   BeamSelectArgs a{};
   a.logits = logits;
   a.ld = ld_logits;

@@ -412,6 +412,13 @@ def _matrix(t: torch.Tensor, what: str):
     return tuple(t.shape)
 
 
+def _workspace(t: torch.Tensor) -> int:
+    """Bytes of a given workspace."""
+    if not t.is_contiguous():
+        raise ValueError("workspace: contiguous elements expected")
+    return t.numel() * t.element_size()
+
+
 def _codes(x, shape, q, scales):
     """Codes and scales for rows like x's, made where not given, and the codes' row stride."""
     if q is None:
@@ -519,7 +526,7 @@ def sample_i8(q: torch.Tensor, q_scales: torch.Tensor, w: torch.Tensor, w_scales
             workspace = torch.empty(max(sample_i8_workspace_bytes(B, D, V), 256), dtype=torch.uint8, device=q.device)
         st = _lib.fs_sample_i8(q.data_ptr(), ldq, q_scales.data_ptr(), w.data_ptr(), ldw, w_scales.data_ptr(),
                                B, D, V, float(temperature), int(seed), int(step), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), out.data_ptr(), _raw_stream(device.index))
+                               _workspace(workspace), out.data_ptr(), _raw_stream(device.index))
     _check(st, "fs_sample_i8")
     return out
 
@@ -570,7 +577,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
         if workspace is None:
             workspace = logits.new_empty(_select_bytes(B, beams, V, n, dt), dtype=torch.uint8)
         st = _lib.fs_beam_select(logits.data_ptr(), ld, dt, scores.data_ptr(), done, int(pad_token), B, beams, V, n,
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 workspace.data_ptr(), _workspace(workspace),
                                  out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _raw_stream(device.index))
     _check(st, "fs_beam_select")
     return tuple(out)

@@ -107,6 +107,8 @@ SELECT = dict(logits=FAKE, ld=1000, dtype=BF16, scores=FAKE, finished=None, pad=
     (dict(logits=FAKE + 2, dtype=F32), UNSUPPORTED), (dict(ws=FAKE + 8), UNSUPPORTED),
     (dict(scores=FAKE + 2), UNSUPPORTED), (dict(s=FAKE + 1), UNSUPPORTED), (dict(p=FAKE + 2), UNSUPPORTED),
     (dict(t=FAKE + 3), UNSUPPORTED), (dict(bytes=100), WS_SMALL),
+    (dict(), INVALID), (dict(s=FAKE + 28), INVALID), (dict(s=FAKE - 60), INVALID),   # scores overwritten in part
+    (dict(n=4, s=FAKE + 4), INVALID),
 ])
 def test_select_refusals(fs, kw, status):
     assert _call(fs._lib.fs_beam_select, SELECT, **kw) == status
@@ -149,6 +151,56 @@ def _reorder(fs, states=(FAKE,), out=None, layout=(2, 4096, 256, 4, 64, 32), out
 ])
 def test_reorder_refusals(fs, kw):
     assert _reorder(fs, **kw) == INVALID
+
+
+def _bytes(at, layout, rows):
+    outer, os, rs, blocks, bs, size = layout
+    return [at + o * os + r * rs + b * bs + i for o in range(outer) for r in range(rows) for b in range(blocks)
+            for i in range(size)]
+
+
+def test_reorder_overlaps_against_bytes():
+    """Random layouts and places: refused just where two buffers, or one with
+    itself, share a byte. Without a device an accepted call ends in a launch
+    error; where there is one, the made-up addresses are not offered."""
+    import random
+
+    import torch
+    if torch.cuda.device_count():
+        pytest.skip("accepted calls would be launched")
+    from lm_head_gemm_amd import flashsample as fs
+    rng = random.Random(5)
+    seen = {True: 0, False: 0}
+    for _ in range(6000):
+        B, beams = rng.randint(1, 2), rng.randint(1, 3)
+        rows = B * beams
+        size = rng.randint(1, 4)
+        counts = [rng.randint(1, 3), rows, rng.randint(1, 3)]
+        strides, span = [0, 0, 0], size
+        for i in rng.sample(range(3), 3):         # dimensions in any order of their strides, mostly apart
+            strides[i] = max(span - (rng.random() < 0.1), 0) + rng.choice([0, 0, 1, 3, 9])
+            span += (counts[i] - 1) * strides[i]
+        layout = (counts[0], strides[0], strides[1], counts[2], strides[2], size)
+        states = [FAKE + rng.randint(0, 3 * span) for _ in range(rng.randint(1, 2))]
+        out = [FAKE + rng.randint(0, 6 * span) for _ in states] if rng.random() < 0.5 else None
+        sets = [_bytes(a, layout, rows) for a in (out or states)]
+        itself = len(set(sets[0])) < len(sets[0])
+        meet = len(sets) > 1 and bool(set(sets[0]) & set(sets[1]))
+        if out:
+            meet = meet or any(set(w) & set(_bytes(a, layout, rows)) for w in sets for a in states)
+        got = _reorder(fs, states, out, layout, B=B, beams=beams)
+        if itself or meet:
+            assert got == INVALID, (layout, rows, states, out)
+        elif got == INVALID:
+            # strides that interleave (no order of dimensions in which each step clears the ones below)
+            order = sorted((s, c) for s, c in zip(strides, counts) if c > 1)
+            below, nested = size, True
+            for s, c in order:
+                nested = nested and s >= below
+                below += (c - 1) * s
+            assert not nested, (layout, rows, states, out)
+        seen[got == INVALID] += 1
+    assert min(seen.values()) > 500
 
 
 def test_reorder_parents_alignment(fs):

@@ -171,6 +171,8 @@ def test_strided_logits_and_given_outputs(fs):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     with pytest.raises(fs.FlashSampleError, match="FS_ERR_WORKSPACE_TOO_SMALL"):
         fs.beam_select(_t(logits), _t(scores), n, workspace=work[:64])
+    with pytest.raises(ValueError, match="workspace"):
+        fs.beam_select(_t(logits), _t(scores), n, workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda")[::2])
     with pytest.raises(fs.FlashSampleError, match="FS_ERR_INVALID_ARGUMENT"):
         fs.beam_select(_t(logits), _t(scores), 65)
     with pytest.raises(fs.FlashSampleError, match="FS_ERR_INVALID_ARGUMENT"):
