@@ -9,7 +9,7 @@
 // no code depends on a sum. What is left is to round an exact quotient: the
 // product u of two 16-bit values is exact in fp32, the product with an fp32
 // gain in fp64. Each code is first taken from fp32 products with 127 / a (off
-// by at most four roundings, 127 x 2^-22 = 3.1e-5 steps); one within 1e-4 of the
+// by at most three roundings, 127 x 3 x 2^-24 = 2.3e-5 steps); one within 1e-4 of the
 // middle between two codes is taken again from the fp64 quotient, whose a is
 // exact: with an fp32 gain, the largest fp64 product among those whose fp32
 // product comes within 2^-22 of the largest. Rows whose largest value fp32
@@ -21,9 +21,9 @@
 // hold V 16-byte pieces each, so a row is read once whatever its length. Gains
 // are fetched beside the row: read between the stores of h and of codes, which
 // no load may pass, they cost 10-40% of the time.
-// Measured: norm with residual, bf16, 4099 x 8192 48.3 us (4.9 TB/s read and
-// written, a large copy's rate), with an fp32 gain 54 us; 64 x 7168 4.8 us, 1 x
-// 4096 3.8 us; codes of 128256 x 4096 bf16 256 us (6.2 TB/s).
+// Measured: norm with residual, bf16, 4099 x 8192 46.5 us (5.1 TB/s read and
+// written, a large copy's rate), with an fp32 gain 52 us; 64 x 7168 4.8 us, 1 x
+// 4096 3.6 us; codes of 128256 x 4096 bf16 254-262 us by box (6.0-6.2 TB/s).
 #include "fs_decode.h"
 
 namespace fs {
@@ -187,12 +187,12 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
   }
 
   int8_t* codes = a.codes + row * a.ldc;
-  auto store = [&](int p, const int (&c)[E]) {
+  auto store = [&](int p, const uint32_t (&c)[E]) {   // the lowest byte of each
     uint32_t w[E / 4];
 #pragma unroll
     for (int k = 0; k < E / 4; ++k)
-      w[k] = (uint32_t)(c[4 * k] & 255) | ((uint32_t)(c[4 * k + 1] & 255) << 8) |
-             ((uint32_t)(c[4 * k + 2] & 255) << 16) | ((uint32_t)(c[4 * k + 3] & 255) << 24);
+      w[k] = __builtin_amdgcn_perm(c[4 * k + 1], c[4 * k], 0x0C0C0400u) |
+             __builtin_amdgcn_perm(c[4 * k + 3], c[4 * k + 2], 0x04000C0Cu);
     if constexpr (E == 8) *reinterpret_cast<uint2*>(codes + (int64_t)p * E) = make_uint2(w[0], w[E / 4 - 1]);
     else *reinterpret_cast<uint32_t*>(codes + (int64_t)p * E) = w[0];
   };
@@ -233,13 +233,21 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
       for (int v = 0; v < V; ++v) {
         const int p = tid + v * G;
         if (p < np) {
-          int c[E];
+          // x + 1.5 2^23 is x rounded to a whole number, which is in the lowest bits
+          constexpr float kWhole = 12582912.0f;
+          uint32_t c[E];
+          float far = 0.0f;   // largest distance from a whole number
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float t = value(v, e, p) * inv;
-            float k = rintf(t);
-            if (fabsf(t - k) > 0.4999f) k = (float)rint(127.0 * (GAIN == 2 ? exact(v, e, p) : (double)value(v, e, p)) / amax);
-            c[e] = (int)k;
+            const float x32 = value(v, e, p), k = fmaf(x32, inv, kWhole);
+            far = fmaxf(far, fabsf(fmaf(x32, inv, kWhole - k)));
+            c[e] = __float_as_uint(k);
+          }
+          if (far > 0.4999f) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (fabsf(fmaf(value(v, e, p), inv, kWhole - __uint_as_float(c[e]))) > 0.4999f)
+                c[e] = (uint32_t)(int)rint(127.0 * (GAIN == 2 ? exact(v, e, p) : (double)value(v, e, p)) / amax);
           }
           store(p, c);
         }
@@ -259,14 +267,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rows_i8_kernel(RowsI8Args a
   for (int v = 0; v < V; ++v) {
     const int p = tid + v * G;
     if (p < np) {
-      int c[E];
+      uint32_t c[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const double x64 = exact(v, e, p);
         const double t = x64 * inv;
         double k = rint(t);
         if (fabs(t - k) > 0.4999) k = rint(127.0 * x64 / amax);
-        c[e] = none ? 0 : (int)k;
+        c[e] = none ? 0u : (uint32_t)(int)k;
       }
       store(p, c);
     }
